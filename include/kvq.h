@@ -74,9 +74,11 @@ extern "C" {
 /* 1: the first release.  2: kvq_config.flags (formerly a reserved field
  * that had to be 0) accepts KVQ_FLAG_EARLY_READS; a caller that sets it can
  * check kvq_abi_version() >= 2 first, as a version-1 library refuses any
- * nonzero value with KVQ_ERR_INVALID_ARG.  The layout of every struct is
- * unchanged. */
-#define KVQ_ABI_VERSION 2
+ * nonzero value with KVQ_ERR_INVALID_ARG.  3: kvq_read, the sink entry points
+ * (kvq_append_sink, kvq_sink_decode, kvq_append_sink_decode) and
+ * kvq_prefill_attention, with the status bit KVQ_DEV_TIMEOUT.  The layout of
+ * every struct is unchanged. */
+#define KVQ_ABI_VERSION 3
 
 /* A cudaStream_t.  NULL means the legacy default stream. */
 typedef struct CUstream_st* kvq_stream_t;
@@ -96,6 +98,7 @@ typedef enum kvq_status {
 #define KVQ_DEV_BAD_POS 2         /* a position past the block table or the RoPE table */
 #define KVQ_DEV_BAD_SEQ 4         /* a sequence id outside [0, n_seqs) */
 #define KVQ_DEV_BAD_LEN 8         /* a seq_len < 0 or past the block table's capacity */
+#define KVQ_DEV_TIMEOUT 16        /* a bounded wait inside a kernel ran out: its output is not valid */
 
 typedef enum kvq_float { KVQ_F32 = 0, KVQ_F16 = 1, KVQ_BF16 = 2 } kvq_float;
 
@@ -380,6 +383,125 @@ kvq_status kvq_append_window_decode(const kvq_config* cfg, int32_t batch, const 
                                     const float* rope_tab, int32_t rope_max_pos,
                                     void* out, void* workspace, size_t workspace_bytes,
                                     int32_t chunk_tokens, int32_t* dev_status, kvq_stream_t stream);
+
+/* ------------------------------------------------------ reading rows back --
+ * The stored rows as numbers: k_out[i] and v_out[i] are K^ and V^ of token
+ * pos[i] of sequence seq_ids[i] (all kv heads), computed in fp32 as s*code
+ * (+ bias, one fused multiply-add) and rounded once to act_dtype; a value past
+ * act_dtype's range becomes infinite.  K comes back as it is stored, rotated
+ * at its position.  For moving rows out of the cache: off-loading, storing
+ * them in another format, handing a prefix to another program.
+ *   seq_ids, pos, block_table, n_seqs, max_pages_per_seq, ring_rows
+ *                 as for kvq_append
+ *   sinks         as for kvq_append_sink; used with ring_rows > 0 only
+ *   k_out, v_out  device [n_rows][n_kv_heads][head_dim] of act_dtype, 16-byte
+ *                 aligned (KVQ_ERR_INVALID_ARG otherwise); one of them may be
+ *                 NULL and is then not read
+ * A row with a bad sequence, position or page sets its bit and its output is
+ * left as it was.  The same row may be asked for any number of times. */
+kvq_status kvq_read(const kvq_config* cfg, int32_t n_rows,
+                    const int32_t* seq_ids, const int32_t* pos,
+                    const int32_t* block_table, int32_t n_seqs,
+                    int32_t max_pages_per_seq, int32_t ring_rows, int32_t sinks,
+                    const void* k_pool, const void* v_pool, int32_t n_pool_pages,
+                    void* k_out, void* v_out, int32_t* dev_status, kvq_stream_t stream);
+
+/* ------------------------------------- window decode with first tokens kept --
+ * Decode attention over a sliding window that also keeps the first `sinks`
+ * tokens of the sequence in sight: the query at position L - 1 attends the
+ * keys t < sinks and the keys t in [max(0, L - window), L).
+ *
+ * Two layouts.  ring_rows == 0: an append-only table, token t in row t.
+ * ring_rows = R > 0: the first PP = ceil(sinks / page_size) pages of a
+ * sequence's table are pinned and hold tokens [0, PP*page_size) for good; the
+ * R rows after them are a ring for the rest:
+ *   row(t) = t                                      t < PP*page_size
+ *   row(t) = PP*page_size + (t - PP*page_size) mod R  otherwise
+ * so the table needs PP + R / page_size entries.  With sinks == 0 this is the
+ * ring of kvq_append and kvq_window_decode.
+ *
+ * kvq_append_sink is kvq_append for this layout (with ring_rows == 0 or
+ * sinks == 0 the two write the same rows). */
+kvq_status kvq_append_sink(const kvq_config* cfg, int32_t n_rows,
+                           const void* k_new, const void* v_new,
+                           const int32_t* seq_ids, const int32_t* pos,
+                           const int32_t* block_table, int32_t n_seqs,
+                           int32_t max_pages_per_seq, int32_t ring_rows, int32_t sinks,
+                           const float* rope_tab, int32_t rope_max_pos,
+                           void* k_pool, void* v_pool, int32_t n_pool_pages,
+                           int32_t* dev_status, kvq_stream_t stream);
+
+/*   block_table   device int32 [batch][max_pages_per_seq]
+ *   ring_rows     0, or a multiple of page_size that fits the table beside the
+ *                 pinned pages
+ *   sinks         >= 0
+ *   window        >= 1, and <= ring_rows with a ring
+ *   workspace     at least kvq_sink_workspace_bytes() with the same batch,
+ *                 max_pages_per_seq, ring_rows, sinks, window and chunk_tokens
+ * All other arguments, and what a bad length or page does, as in
+ * kvq_decode_attention.  KVQ_FLAG_EARLY_READS is accepted; with sinks > 0
+ * everything is read after the wait. */
+size_t kvq_sink_workspace_bytes(const kvq_config* cfg, int32_t batch, int32_t max_pages_per_seq,
+                                int32_t ring_rows, int32_t sinks, int32_t window, int32_t chunk_tokens);
+kvq_status kvq_sink_decode(const kvq_config* cfg, int32_t batch, const void* q,
+                           const void* k_pool, const void* v_pool, int32_t n_pool_pages,
+                           const int32_t* block_table, int32_t max_pages_per_seq,
+                           int32_t ring_rows, int32_t sinks, int32_t window,
+                           const int32_t* seq_lens, const float* rope_tab, int32_t rope_max_pos,
+                           void* out, void* workspace, size_t workspace_bytes,
+                           int32_t chunk_tokens, int32_t* dev_status, kvq_stream_t stream);
+/* The fused step: kvq_append_sink of row b at pos[b] into sequence b, then
+ * kvq_sink_decode (k_new, v_new and pos as in kvq_append_decode_attention). */
+kvq_status kvq_append_sink_decode(const kvq_config* cfg, int32_t batch, const void* q,
+                                  const void* k_new, const void* v_new, const int32_t* pos,
+                                  void* k_pool, void* v_pool, int32_t n_pool_pages,
+                                  const int32_t* block_table, int32_t max_pages_per_seq,
+                                  int32_t ring_rows, int32_t sinks, int32_t window,
+                                  const int32_t* seq_lens, const float* rope_tab, int32_t rope_max_pos,
+                                  void* out, void* workspace, size_t workspace_bytes,
+                                  int32_t chunk_tokens, int32_t* dev_status, kvq_stream_t stream);
+
+/* ------------------------------------------------------ prefill attention --
+ * Causal attention of the last n_b tokens of every sequence b over its cache,
+ * which already holds them (kvq_append or kvq_append_sink of the chunk comes
+ * first): whole prompts, chunks of a prompt, drafted tokens to verify.  With
+ * L = seq_lens[b], n_b = q_starts[b+1] - q_starts[b] and query row
+ * q_starts[b] + i at position p = L - n_b + i:
+ *   q~  = RoPE(q[row][h]) at position p
+ *   out[row][h] = sum_t softmax(alpha * <q~, K^_t>)_t V^_t
+ *   over t <= p with window == 0, or t > p - window, or t < sinks
+ *   n_rows        rows of q and out
+ *   q, out        device [n_rows][n_heads][head_dim] of act_dtype, 16-byte aligned
+ *   q_starts      device int32 [batch + 1], non-decreasing, within [0, n_rows]:
+ *                 the first row of each sequence, and the end of the last.
+ *                 n_b may be 0.  Rows no sequence owns are left as they were
+ *   window        0: the whole context.  >= 1: the sliding window
+ *   sinks, ring_rows  as for kvq_sink_decode; sinks needs a window, and a ring
+ *                 a window of at most ring_rows.  The ring must still hold what
+ *                 the first query attends: n_b + window - 1 <= ring_rows is enough
+ *   workspace     device scratch of at least kvq_prefill_workspace_bytes() with
+ *                 the same arguments, 256-byte aligned.  It needs no clearing
+ * With f16 or bf16 activations and scale groups of at least 32 elements the
+ * products run on the tensor cores with operands rounded to fp16 (the rotated
+ * query, K^, V^ and the softmax weights, each held at a power-of-two scale
+ * that keeps it inside fp16's range) and fp32 sums; otherwise everything is
+ * fp32.  A query row that attends a token whose stored K or V is not finite
+ * is NaN; other rows are not touched by it.
+ * q_starts that are not in order set KVQ_DEV_BAD_SEQ and their sequence's rows
+ * are left out.  A length that is bad, shorter than n_b, or whose ring rows are
+ * already overwritten sets KVQ_DEV_BAD_LEN; one past the RoPE table sets
+ * KVQ_DEV_BAD_POS; the sequence's rows are then zero.  A bad page id sets
+ * KVQ_DEV_BAD_PAGE and its tokens are left out. */
+size_t kvq_prefill_workspace_bytes(const kvq_config* cfg, int32_t batch, int32_t n_rows,
+                                   int32_t max_pages_per_seq, int32_t ring_rows, int32_t sinks,
+                                   int32_t window);
+kvq_status kvq_prefill_attention(const kvq_config* cfg, int32_t batch, int32_t n_rows, const void* q,
+                                 const int32_t* q_starts, const void* k_pool, const void* v_pool,
+                                 int32_t n_pool_pages, const int32_t* block_table,
+                                 int32_t max_pages_per_seq, int32_t ring_rows, int32_t sinks,
+                                 int32_t window, const int32_t* seq_lens, const float* rope_tab,
+                                 int32_t rope_max_pos, void* out, void* workspace,
+                                 size_t workspace_bytes, int32_t* dev_status, kvq_stream_t stream);
 
 /* ------------------------------------------- decode without allocation --
  * The pages have no counterpart to this entry point.  It exists for callers

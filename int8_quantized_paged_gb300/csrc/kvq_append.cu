@@ -28,7 +28,7 @@ struct AppendArgs {
   uint8_t* k_pool;
   uint8_t* v_pool;
   int32_t* status;
-  int32_t n_rows, n_kv_heads, n_seqs, max_pages, ring_rows, rope_max_pos, n_pool_pages;
+  int32_t n_rows, n_kv_heads, n_seqs, max_pages, ring_rows, pin_rows, rope_max_pos, n_pool_pages;
   int32_t act, rope;
   PoolLayout kl, vl;
 };
@@ -55,7 +55,7 @@ __global__ void __launch_bounds__(128) append_kernel(const AppendArgs a) {
     if (lane == 0 && head == 0) report(a.status, KVQ_DEV_BAD_SEQ);
     return;
   }
-  const int r = a.ring_rows > 0 ? (pos >= 0 ? pos % a.ring_rows : -1) : pos;
+  const int r = pos >= 0 ? row_of(pos, a.ring_rows, a.pin_rows) : -1;
   if (pos < 0 || r / P >= a.max_pages || (a.rope != KVQ_ROPE_NONE && pos >= a.rope_max_pos)) {
     if (lane == 0 && head == 0) report(a.status, KVQ_DEV_BAD_POS);
     return;
@@ -84,18 +84,11 @@ __global__ void __launch_bounds__(128) append_kernel(const AppendArgs a) {
             a.v_pool + (int64_t)page * a.vl.page_bytes + (int64_t)head * a.vl.sub_bytes, slot, lane);
 }
 
-}  // namespace kvq
-
-using namespace kvq;
-
-extern "C" kvq_status kvq_append(const kvq_config* cfg, int32_t n_rows, const void* k_new,
-                                 const void* v_new, const int32_t* seq_ids, const int32_t* pos,
-                                 const int32_t* block_table, int32_t n_seqs,
-                                 int32_t max_pages_per_seq, int32_t ring_rows,
-                                 const float* rope_tab, int32_t rope_max_pos, void* k_pool,
-                                 void* v_pool, int32_t n_pool_pages, int32_t* dev_status,
-                                 kvq_stream_t stream) {
-  clear_error();
+static kvq_status run_append(const kvq_config* cfg, int32_t n_rows, const void* k_new, const void* v_new,
+                             const int32_t* seq_ids, const int32_t* pos, const int32_t* block_table,
+                             int32_t n_seqs, int32_t max_pages_per_seq, int32_t ring_rows, int32_t sinks,
+                             const float* rope_tab, int32_t rope_max_pos, void* k_pool, void* v_pool,
+                             int32_t n_pool_pages, int32_t* dev_status, kvq_stream_t stream) {
   kvq_status st = check_kernel_config(cfg);
   if (st != KVQ_OK) return st;
   if (n_rows < 0) return fail(KVQ_ERR_INVALID_ARG, "n_rows (%d) < 0", n_rows);
@@ -106,9 +99,8 @@ extern "C" kvq_status kvq_append(const kvq_config* cfg, int32_t n_rows, const vo
     return fail(KVQ_ERR_INVALID_ARG, "n_seqs, max_pages_per_seq and n_pool_pages must be >= 1");
   if (!seq_ids && n_rows > n_seqs)
     return fail(KVQ_ERR_INVALID_ARG, "without seq_ids, n_rows (%d) must be <= n_seqs (%d)", n_rows, n_seqs);
-  if (ring_rows < 0 || ring_rows % cfg->page_size != 0 || ring_rows / cfg->page_size > max_pages_per_seq)
-    return fail(KVQ_ERR_INVALID_ARG, "ring_rows %d must be a multiple of page_size that fits the table",
-                ring_rows);
+  st = check_layout(*cfg, max_pages_per_seq, ring_rows, sinks);
+  if (st != KVQ_OK) return st;
   if (cfg->rope != KVQ_ROPE_NONE && (!rope_tab || rope_max_pos < 1))
     return fail(KVQ_ERR_INVALID_ARG, "RoPE config needs rope_tab and rope_max_pos >= 1");
   if ((reinterpret_cast<uintptr_t>(k_pool) | reinterpret_cast<uintptr_t>(v_pool)) & 15)
@@ -120,7 +112,8 @@ extern "C" kvq_status kvq_append(const kvq_config* cfg, int32_t n_rows, const vo
   a.k_pool = static_cast<uint8_t*>(k_pool); a.v_pool = static_cast<uint8_t*>(v_pool);
   a.status = dev_status;
   a.n_rows = n_rows; a.n_kv_heads = cfg->n_kv_heads; a.n_seqs = n_seqs;
-  a.max_pages = max_pages_per_seq; a.ring_rows = ring_rows; a.rope_max_pos = rope_max_pos;
+  a.max_pages = max_pages_per_seq; a.ring_rows = ring_rows;
+  a.pin_rows = pinned_rows(*cfg, ring_rows, sinks); a.rope_max_pos = rope_max_pos;
   a.n_pool_pages = n_pool_pages; a.act = cfg->act_dtype; a.rope = cfg->rope;
   a.kl = pool_layout(*cfg, 0);
   a.vl = pool_layout(*cfg, 1);
@@ -148,4 +141,32 @@ extern "C" kvq_status kvq_append(const kvq_config* cfg, int32_t n_rows, const vo
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return fail(KVQ_ERR_CUDA, "append launch: %s", cudaGetErrorString(e));
   return KVQ_OK;
+}
+
+}  // namespace kvq
+
+using namespace kvq;
+
+extern "C" kvq_status kvq_append(const kvq_config* cfg, int32_t n_rows, const void* k_new,
+                                 const void* v_new, const int32_t* seq_ids, const int32_t* pos,
+                                 const int32_t* block_table, int32_t n_seqs,
+                                 int32_t max_pages_per_seq, int32_t ring_rows,
+                                 const float* rope_tab, int32_t rope_max_pos, void* k_pool,
+                                 void* v_pool, int32_t n_pool_pages, int32_t* dev_status,
+                                 kvq_stream_t stream) {
+  clear_error();
+  return run_append(cfg, n_rows, k_new, v_new, seq_ids, pos, block_table, n_seqs, max_pages_per_seq, ring_rows, 0,
+                    rope_tab, rope_max_pos, k_pool, v_pool, n_pool_pages, dev_status, stream);
+}
+
+extern "C" kvq_status kvq_append_sink(const kvq_config* cfg, int32_t n_rows, const void* k_new,
+                                      const void* v_new, const int32_t* seq_ids, const int32_t* pos,
+                                      const int32_t* block_table, int32_t n_seqs,
+                                      int32_t max_pages_per_seq, int32_t ring_rows, int32_t sinks,
+                                      const float* rope_tab, int32_t rope_max_pos, void* k_pool,
+                                      void* v_pool, int32_t n_pool_pages, int32_t* dev_status,
+                                      kvq_stream_t stream) {
+  clear_error();
+  return run_append(cfg, n_rows, k_new, v_new, seq_ids, pos, block_table, n_seqs, max_pages_per_seq, ring_rows,
+                    sinks, rope_tab, rope_max_pos, k_pool, v_pool, n_pool_pages, dev_status, stream);
 }

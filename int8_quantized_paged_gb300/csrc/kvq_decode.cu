@@ -287,7 +287,7 @@ static kvq_status run_decode(const kvq_config* cfg, int32_t batch, const void* q
                              int32_t chunk_tokens, int32_t* dev_status, cudaStream_t stream,
                              int32_t ring_rows, int32_t window, int64_t max_tokens,
                              const void* app_k = nullptr, const void* app_v = nullptr,
-                             const int32_t* app_pos = nullptr) {
+                             const int32_t* app_pos = nullptr, int32_t sinks = 0) {
   const Plan w = make_plan(*cfg, batch, max_tokens, window > 0, chunk_tokens);
   if (w.n_chunks > kMaxChunks)
     return fail(KVQ_ERR_INVALID_ARG, "%d chunks exceed the limit %d; use larger chunks", w.n_chunks, kMaxChunks);
@@ -317,6 +317,8 @@ static kvq_status run_decode(const kvq_config* cfg, int32_t batch, const void* q
   a.rope_max_pos = rope_max_pos;
   a.ring_rows = ring_rows;
   a.window = window;
+  a.sinks = sinks;
+  a.pin_rows = pinned_rows(*cfg, ring_rows, sinks);
   a.chunk_tokens = w.chunk_tokens;
   a.n_chunks = w.n_chunks;
   a.act = cfg->act_dtype;
@@ -581,4 +583,102 @@ extern "C" kvq_status kvq_window_decode(const kvq_config* cfg, int32_t batch, co
   return run_decode(cfg, batch, q, k_pool, v_pool, n_pool_pages, ring_table, ring_rows / cfg->page_size,
                     seq_lens, rope_tab, rope_max_pos, out, workspace, workspace_bytes, chunk_tokens,
                     dev_status, (cudaStream_t)stream, ring_rows, window, window);
+}
+
+// Tokens (rounded up to whole blocks for the sinks) one windowed query attends
+// at most: what the chunk plan and the cluster choice go by.
+static int64_t sink_span(const kvq_config& c, int32_t max_pages, int32_t ring_rows, int32_t sinks, int32_t window) {
+  const int64_t P = c.page_size, cap = (int64_t)max_pages * P;
+  const int64_t first = ((int64_t)sinks + P - 1) / P * P;
+  if (ring_rows > 0) return first + window;
+  return first + window < cap ? first + window : cap;
+}
+
+// Checks of the window-with-sinks layout shared by its entry points.
+static kvq_status check_sink_layout(const kvq_config& c, int32_t max_pages, int32_t ring_rows, int32_t sinks,
+                                    int32_t window) {
+  if (max_pages < 1) return fail(KVQ_ERR_INVALID_ARG, "max_pages_per_seq must be >= 1");
+  const kvq_status st = check_layout(c, max_pages, ring_rows, sinks);
+  if (st != KVQ_OK) return st;
+  if (window < 1 || (ring_rows > 0 && window > ring_rows))
+    return fail(KVQ_ERR_INVALID_ARG, "window %d must be >= 1, and with a ring at most ring_rows=%d", window, ring_rows);
+  return KVQ_OK;
+}
+
+extern "C" size_t kvq_sink_workspace_bytes(const kvq_config* cfg, int32_t batch, int32_t max_pages_per_seq,
+                                           int32_t ring_rows, int32_t sinks, int32_t window, int32_t chunk_tokens) {
+  clear_error();
+  if (check_kernel_config(cfg) != KVQ_OK) return 0;
+  if (batch < 0 || chunk_tokens < 0 || chunk_tokens % cfg->page_size) {
+    set_error("bad batch or chunk_tokens");
+    return 0;
+  }
+  if (check_sink_layout(*cfg, max_pages_per_seq, ring_rows, sinks, window) != KVQ_OK) return 0;
+  return make_plan(*cfg, batch, sink_span(*cfg, max_pages_per_seq, ring_rows, sinks, window), true, chunk_tokens).total;
+}
+
+static kvq_status run_sink(const kvq_config* cfg, int32_t batch, const void* q, const void* k_pool,
+                           const void* v_pool, int32_t n_pool_pages, const int32_t* block_table,
+                           int32_t max_pages_per_seq, int32_t ring_rows, int32_t sinks, int32_t window,
+                           const int32_t* seq_lens, const float* rope_tab, int32_t rope_max_pos, void* out,
+                           void* workspace, size_t workspace_bytes, int32_t chunk_tokens, int32_t* dev_status,
+                           kvq_stream_t stream, const void* k_new, const void* v_new, const int32_t* pos) {
+  return run_decode(cfg, batch, q, k_pool, v_pool, n_pool_pages, block_table, max_pages_per_seq, seq_lens, rope_tab,
+                    rope_max_pos, out, workspace, workspace_bytes, chunk_tokens, dev_status, (cudaStream_t)stream,
+                    ring_rows, window, sink_span(*cfg, max_pages_per_seq, ring_rows, sinks, window), k_new, v_new,
+                    pos, sinks);
+}
+
+extern "C" kvq_status kvq_sink_decode(const kvq_config* cfg, int32_t batch, const void* q, const void* k_pool,
+                                      const void* v_pool, int32_t n_pool_pages, const int32_t* block_table,
+                                      int32_t max_pages_per_seq, int32_t ring_rows, int32_t sinks, int32_t window,
+                                      const int32_t* seq_lens, const float* rope_tab, int32_t rope_max_pos,
+                                      void* out, void* workspace, size_t workspace_bytes, int32_t chunk_tokens,
+                                      int32_t* dev_status, kvq_stream_t stream) {
+  clear_error();
+  kvq_status st = check_decode_args(cfg, batch, q, k_pool, v_pool, n_pool_pages, block_table, seq_lens,
+                                    rope_tab, rope_max_pos, out, workspace, chunk_tokens, dev_status);
+  if (st != KVQ_OK || batch == 0) return st;
+  st = check_sink_layout(*cfg, max_pages_per_seq, ring_rows, sinks, window);
+  if (st != KVQ_OK) return st;
+  return run_sink(cfg, batch, q, k_pool, v_pool, n_pool_pages, block_table, max_pages_per_seq, ring_rows, sinks,
+                  window, seq_lens, rope_tab, rope_max_pos, out, workspace, workspace_bytes, chunk_tokens, dev_status,
+                  stream, nullptr, nullptr, nullptr);
+}
+
+extern "C" kvq_status kvq_append_sink_decode(const kvq_config* cfg, int32_t batch, const void* q,
+                                             const void* k_new, const void* v_new, const int32_t* pos,
+                                             void* k_pool, void* v_pool, int32_t n_pool_pages,
+                                             const int32_t* block_table, int32_t max_pages_per_seq,
+                                             int32_t ring_rows, int32_t sinks, int32_t window,
+                                             const int32_t* seq_lens, const float* rope_tab, int32_t rope_max_pos,
+                                             void* out, void* workspace, size_t workspace_bytes,
+                                             int32_t chunk_tokens, int32_t* dev_status, kvq_stream_t stream) {
+  clear_error();
+  kvq_status st = check_decode_args(cfg, batch, q, k_pool, v_pool, n_pool_pages, block_table, seq_lens,
+                                    rope_tab, rope_max_pos, out, workspace, chunk_tokens, dev_status);
+  if (st != KVQ_OK || batch == 0) return st;
+  st = check_sink_layout(*cfg, max_pages_per_seq, ring_rows, sinks, window);
+  if (st != KVQ_OK) return st;
+  if (!k_new || !v_new || !pos) return fail(KVQ_ERR_INVALID_ARG, "k_new, v_new and pos must not be NULL");
+  if ((reinterpret_cast<uintptr_t>(k_new) | reinterpret_cast<uintptr_t>(v_new)) & 15)
+    return fail(KVQ_ERR_INVALID_ARG, "k_new and v_new must be 16-byte aligned");
+  if (!tc_enabled(*cfg)) {
+    // The CUDA-core decode has no fused append: the append kernel, then the
+    // decode, whose own refusals come first, so that nothing is enqueued then.
+    const Plan w = make_plan(*cfg, batch, sink_span(*cfg, max_pages_per_seq, ring_rows, sinks, window), true,
+                             chunk_tokens);
+    if (w.n_chunks > kMaxChunks || workspace_bytes < w.total || batch > 65535 || cfg->n_kv_heads > 65535)
+      return run_sink(cfg, batch, q, k_pool, v_pool, n_pool_pages, block_table, max_pages_per_seq, ring_rows, sinks,
+                      window, seq_lens, rope_tab, rope_max_pos, out, workspace, workspace_bytes, chunk_tokens,
+                      dev_status, stream, nullptr, nullptr, nullptr);
+    st = kvq_append_sink(cfg, batch, k_new, v_new, nullptr, pos, block_table, batch, max_pages_per_seq, ring_rows,
+                         sinks, rope_tab, rope_max_pos, k_pool, v_pool, n_pool_pages, dev_status, stream);
+    if (st != KVQ_OK) return st;
+    k_new = v_new = nullptr;
+    pos = nullptr;
+  }
+  return run_sink(cfg, batch, q, k_pool, v_pool, n_pool_pages, block_table, max_pages_per_seq, ring_rows, sinks,
+                  window, seq_lens, rope_tab, rope_max_pos, out, workspace, workspace_bytes, chunk_tokens, dev_status,
+                  stream, k_new, v_new, pos);
 }

@@ -52,6 +52,8 @@ struct DecodeArgs {
   int32_t batch, n_heads, n_kv_heads, n_pool_pages, max_pages, rope_max_pos;
   int32_t ring_rows;      // 0: append-only
   int32_t window;         // 0: whole context
+  int32_t sinks;          // with a window: the first tokens that stay visible
+  int32_t pin_rows;       // rows pinned in front of a ring for them (row_of)
   int32_t chunk_tokens, n_chunks;
   int32_t act, rope;
   float score_scale;      // alpha * log2(e)
@@ -61,6 +63,9 @@ struct DecodeArgs {
 __host__ __device__ constexpr int cmin(int a, int b) { return a < b ? a : b; }
 __host__ __device__ constexpr int cmax(int a, int b) { return a > b ? a : b; }
 
+// First tokens a windowed query attends beside its window [lo, L).
+__device__ __forceinline__ int sink_tokens(const DecodeArgs& a, int lo) { return min(a.sinks, lo); }
+
 // Length checks shared by the decode and combine kernels.  Returns the number
 // of attended tokens, or -1 (with the bit to report) for a bad length.
 __device__ __forceinline__ int attended(const DecodeArgs& a, int L, int* lo, int* bad) {
@@ -69,7 +74,7 @@ __device__ __forceinline__ int attended(const DecodeArgs& a, int L, int* lo, int
   if (L < 0 || L > cap) { *bad = KVQ_DEV_BAD_LEN; return -1; }
   if (L > 0 && a.rope != KVQ_ROPE_NONE && L - 1 >= a.rope_max_pos) { *bad = KVQ_DEV_BAD_POS; return -1; }
   *lo = a.window > 0 ? max(0, L - a.window) : 0;
-  return L - *lo;
+  return L - *lo + sink_tokens(a, *lo);
 }
 
 template <int KK, int VK, int HD, int G>
@@ -106,9 +111,12 @@ __global__ void __launch_bounds__(128) decode_chunk_kernel(const DecodeArgs a) {
     if (threadIdx.x == 0 && chunk == 0 && kvh == 0) report(a.status, bad);
     return;
   }
-  const int t0 = lo + chunk * a.chunk_tokens;
-  if (chunk * a.chunk_tokens >= n_att) return;        // empty chunk: never combined
-  const int t1 = min(L, t0 + a.chunk_tokens);
+  // The attended tokens, counted 0 .. n_att - 1: the sinks, then the window.
+  const int t0 = chunk * a.chunk_tokens;
+  if (t0 >= n_att) return;        // empty chunk: never combined
+  const int t1 = min(n_att, t0 + a.chunk_tokens);
+  const int n_sink = sink_tokens(a, lo);
+  auto token = [&](int i) { return i < n_sink ? i : i - n_sink + lo; };
 
   // Rotate the G queries at position L-1 (fp32) and fold in the score scale.
   {
@@ -182,7 +190,7 @@ __global__ void __launch_bounds__(128) decode_chunk_kernel(const DecodeArgs a) {
 #pragma unroll
       for (int h = 0; h < G; ++h) sc[h] = 0.f;
       if (valid) {
-        const int row = a.ring_rows > 0 ? t % a.ring_rows : t;
+        const int row = row_of(token(t), a.ring_rows, a.pin_rows);
         const int page = bt[row / P];
         const int slot = row % P;
         if (page < 0 || page >= a.n_pool_pages) {
@@ -265,8 +273,7 @@ __global__ void __launch_bounds__(128) decode_chunk_kernel(const DecodeArgs a) {
         any |= p[h] != 0.f;
       }
       if (any) {  // p > 0 only for tokens whose page id was checked above
-        const int t = tb + tt;
-        const int row = a.ring_rows > 0 ? t % a.ring_rows : t;
+        const int row = row_of(token(tb + tt), a.ring_rows, a.pin_rows);
         const int page = bt[row / P];
         const int slot = row % P;
         const uint8_t* sub = vbase + (int64_t)page * a.vl.page_bytes;

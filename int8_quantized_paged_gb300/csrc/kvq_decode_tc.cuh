@@ -65,6 +65,8 @@
 
 namespace kvq {
 
+constexpr int kTcPlain = 0, kTcEarly = 1, kTcSink = 2;
+
 struct TcArgs {
   DecodeArgs d;
   void* out;
@@ -262,11 +264,17 @@ __device__ __forceinline__ float hilo_part_unscaled(float x, int part) {
 // PT: stored type of the scales (and biases) of K and V.
 // CL: the cluster mode (kClusterWarps warps per CTA, the chunks of a
 // (sequence, kv head) one cluster of A.cluster CTAs); else kWarps warps.
-template <int KK, int VK, int HD, int NT, int NG, int PT, bool CL, bool EARLY>
+// MODE: kTcPlain, kTcEarly (the early reads described below) or kTcSink (a
+// window with first tokens: blocks 0 .. sb - 1 of the attended list hold the
+// sinks and the rest the window).  A template parameter, as the extra
+// arithmetic per page is not free: a runtime early flag cost the continuous
+// batch 2.7 %.
+template <int KK, int VK, int HD, int NT, int NG, int PT, bool CL, int MODE>
 __global__ void __launch_bounds__(32 * (CL ? kClusterWarps : kWarps),
                                    CL ? tc_cluster_min_blocks(HD) : tc_min_blocks(HD, NT, KK))
 decode_tc_kernel(const __grid_constant__ TcArgs A) {
   constexpr int P = 16;
+  constexpr bool EARLY = MODE == kTcEarly, SINK = MODE == kTcSink;
   constexpr int NW = CL ? kClusterWarps : kWarps;
   constexpr int D = tc_depth(HD, NT, KK, CL);   // pages in flight per warp
   constexpr bool K8 = KK == KVQ_SYM_INT8, V8 = VK == KVQ_SYM_INT8;
@@ -402,13 +410,18 @@ decode_tc_kernel(const __grid_constant__ TcArgs A) {
   // a peer's shared memory makes sure every peer has too
   if constexpr (CL) tc::cluster_arrive_relaxed();
   const int blk_lo = lo / P, blk_hi = (L + P - 1) / P;
-  const int nch = (blk_hi - blk_lo + CB - 1) / CB;
+  // SINK: the attended blocks are the sb blocks of the sinks, then [blk_lo,
+  // blk_hi); where the two meet, they are one run from 0.
+  const int sb = SINK ? min((sink_tokens(a, lo) + P - 1) / P, blk_lo) : 0;
+  const int nch = (blk_hi - blk_lo + sb + CB - 1) / CB;
   // In the cluster mode every CTA of the cluster reaches every cluster
   // barrier below: a CTA past the sequence's last chunk reads no page and
   // contributes an empty partial.
   if (chunk >= nch && !CL) return;
-  const int cb0 = blk_lo + chunk * CB;
-  const int ncb = chunk < nch ? min(CB, blk_hi - cb0) : 0;
+  // first block of the chunk (SINK: its index among the attended blocks)
+  const int cb0 = SINK ? chunk * CB : blk_lo + chunk * CB;
+  const int ncb = chunk < nch ? min(CB, (SINK ? blk_hi - blk_lo + sb : blk_hi) - cb0) : 0;
+  auto block_at = [&](int v) -> int { return SINK && v >= sb ? v - sb + blk_lo : v; };   // absolute block
   const int n_local = w < ncb ? (ncb - w + NW - 1) / NW : 0;   // pages w, w + NW, ... of the chunk
 
   // ---- page ring of this warp: D slots of SLOT bytes.  Lane (hl = lane % 16)
@@ -435,10 +448,16 @@ decode_tc_kernel(const __grid_constant__ TcArgs A) {
   }
   const uint32_t lane_sub = wring + (vlane ? KC : 0);   // f16: this lane's sub-block in slot 0
   const int ring = a.ring_rows, npp = a.n_pool_pages;
+  auto table_index = [&](int blk) -> int {   // block-table entry of an absolute block
+    if constexpr (SINK) {
+      const int pin = a.pin_rows / P;
+      return ring > 0 && blk >= pin ? pin + (blk - pin) % (ring / P) : blk;
+    } else {
+      return ring > 0 ? (int)(((int64_t)blk * P) % ring) / P : blk;
+    }
+  };
   auto page_of = [&](int k) -> int {   // page id of this warp's k-th page (k < n_local)
-    const int blk = cb0 + w + NW * k;
-    const int idx = ring > 0 ? (int)(((int64_t)blk * P) % ring) / P : blk;
-    return bt[idx];
+    return bt[table_index(block_at(cb0 + w + NW * k))];
   };
   auto checked = [&](int pg, int k) -> int {   // -1 (and a flag) for an id outside the pool
     const bool ok = pg >= 0 && pg < npp;
@@ -496,17 +515,18 @@ decode_tc_kernel(const __grid_constant__ TcArgs A) {
     const bool pos_ok = apos >= 0 && (ring > 0 || apos / P < a.max_pages) &&
                         (a.rope == KVQ_ROPE_NONE || apos < a.rope_max_pos);
     const int bp = apos / P;
+    const int vp = SINK && bp >= blk_lo ? bp - blk_lo + sb : bp;   // counted as cb0 is
     bool writer = false;   // this CTA writes the row
     if (!pos_ok) {
       if (chunk == 0 && tid == 0) report(a.status, KVQ_DEV_BAD_POS);
-    } else if (bp >= blk_lo && bp < blk_hi) {
-      writer = chunk == (bp - blk_lo) / CB;
-      if (writer && w == (bp - cb0) % NW) k_app = (bp - cb0) / NW;
+    } else if ((bp >= blk_lo || (SINK && bp < sb)) && bp < blk_hi) {
+      writer = chunk == (SINK ? vp : bp - blk_lo) / CB;
+      if (writer && w == (vp - cb0) % NW) k_app = (vp - cb0) / NW;
     } else {
       writer = chunk == 0;
     }
     if (writer) {
-      app_pg = bt[ring > 0 ? (int)(((int64_t)bp * P) % ring) / P : bp];   // a ring keeps the block in a ring page
+      app_pg = bt[table_index(bp)];   // a ring keeps the block in a ring page
       if (app_pg < 0 || app_pg >= npp) {
         if (tid == 0) report(a.status, KVQ_DEV_BAD_PAGE);
         k_app = -1;
@@ -926,7 +946,7 @@ decode_tc_kernel(const __grid_constant__ TcArgs A) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int t = tb + gid + 8 * j;
-        if (t < lo || t >= L)
+        if ((t < lo && !(SINK && t < a.sinks)) || t >= L)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) sc[nt][j] = -INFINITY;
       }
@@ -984,7 +1004,7 @@ decode_tc_kernel(const __grid_constant__ TcArgs A) {
         if constexpr (VAFF) vb[j] = ld_param<PT>(pr + PB);
         if (edge) {
           const int t = tb + gid + 8 * j;
-          if (t < lo || t >= L) vs[j] = vb[j] = 0.f;
+          if ((t < lo && !(SINK && t < a.sinks)) || t >= L) vs[j] = vb[j] = 0.f;
         }
       }
       float vig = vinv[0];
@@ -1057,11 +1077,31 @@ decode_tc_kernel(const __grid_constant__ TcArgs A) {
       }
     };
     if constexpr (ONEG) weights(0);
+    // f16 rows a page's edge leaves out may hold anything, and 0 * NaN is
+    // NaN: their elements are zeroed (a quantised row's scale is, above).  A
+    // lane's words hold tokens 2tig, 2tig+1 (keep0) and 2tig+8, 2tig+9 (keep1).
+    uint32_t keep0 = ~0u, keep1 = ~0u;
+    if constexpr (F16) {
+      if (edge) {
+        auto half = [&](int i, uint32_t bits) -> uint32_t {
+          const int t = tb + i;
+          return (t < lo && !(SINK && t < a.sinks)) || t >= L ? 0u : bits;
+        };
+        keep0 = half(2 * tig, 0xFFFFu) | half(2 * tig + 1, 0xFFFF0000u);
+        keep1 = half(2 * tig + 8, 0xFFFFu) | half(2 * tig + 9, 0xFFFF0000u);
+      }
+    }
 #pragma unroll
     for (int c2 = 0; c2 < VCH / 2; ++c2) {
       uint32_t y[4];   // (tokens 0-7, chunk c), (8-15, c), (0-7, c+1), (8-15, c+1)
       tc::ldsm_x4_trans(vc + vls[c2], y);
       if constexpr (F16) {
+        if (edge) {
+          y[0] &= keep0;
+          y[1] &= keep1;
+          y[2] &= keep0;
+          y[3] &= keep1;
+        }
         // m-tile c2 (dims of chunks 2c2, 2c2+1): A = V^T as loaded, rows dims
         const uint32_t av[4] = {y[0], y[2], y[1], y[3]};
 #pragma unroll
@@ -1087,7 +1127,7 @@ decode_tc_kernel(const __grid_constant__ TcArgs A) {
       }
     }
   };
-  auto tok0 = [&](int k) { return (cb0 + w + k * NW) * P; };   // absolute token of row 0 of page k
+  auto tok0 = [&](int k) { return block_at(cb0 + w + k * NW) * P; };   // absolute token of row 0 of page k
   auto is_edge = [&](int tb) { return tb < lo || tb + P > L; };
   // The whole page k in slot sl.
   auto one_page = [&](int k, int sl) {
@@ -1502,9 +1542,9 @@ struct TcLaunchCfg {
 };
 
 // Host launcher of one instantiation.
-template <int KK, int VK, int HD, int NT, int NG, int PT, bool CL, bool EARLY>
+template <int KK, int VK, int HD, int NT, int NG, int PT, bool CL, int MODE>
 kvq_status launch_tc_one(const TcArgs& t, const TcLaunchCfg& lc) {
-  auto kern = decode_tc_kernel<KK, VK, HD, NT, NG, PT, CL, EARLY>;
+  auto kern = decode_tc_kernel<KK, VK, HD, NT, NG, PT, CL, MODE>;
   static bool attr_done[64] = {false};
   int dev = 0;
   cudaGetDevice(&dev);
@@ -1562,6 +1602,15 @@ inline bool tc_has_shape(int head_dim, int nt, int ng) {
   return ng_ok && head_dim / ng >= 32 && (head_dim == 128 || ((head_dim == 64 || head_dim == 256) && nt == 1));
 }
 
+// Sinks have their own instantiation, which reads everything after the wait
+// (the early flag is a permission); without sinks a window runs as before.
+template <int KK, int VK, int HD, int NT, int NG, int PT, bool CL>
+kvq_status launch_tc_mode(const TcArgs& t, const TcLaunchCfg& lc) {
+  if (t.d.sinks > 0) return launch_tc_one<KK, VK, HD, NT, NG, PT, CL, kTcSink>(t, lc);
+  return t.early ? launch_tc_one<KK, VK, HD, NT, NG, PT, CL, kTcEarly>(t, lc)
+                 : launch_tc_one<KK, VK, HD, NT, NG, PT, CL, kTcPlain>(t, lc);
+}
+
 template <int KK, int VK, int PT>
 kvq_status launch_tc_pt(const TcArgs& t, int head_dim, int nt, int ng, const TcLaunchCfg& lc) {
 #define KVQ_TC(HD_, NT_, NG_)                                                                      \
@@ -1569,11 +1618,9 @@ kvq_status launch_tc_pt(const TcArgs& t, int head_dim, int nt, int ng, const TcL
     if (head_dim == HD_ && nt == NT_ && ng == NG_) {                                               \
       if constexpr (tc_cluster_shape(HD_, NT_))                                                     \
         if (lc.cluster > 0)                                                                        \
-          return t.early ? launch_tc_one<KK, VK, HD_, NT_, NG_, PT, true, true>(t, lc)             \
-                         : launch_tc_one<KK, VK, HD_, NT_, NG_, PT, true, false>(t, lc);           \
+          return launch_tc_mode<KK, VK, HD_, NT_, NG_, PT, true>(t, lc);                           \
       if (lc.cluster > 0) return fail(KVQ_ERR_UNSUPPORTED, "no cluster-mode kernel for this shape"); \
-      return t.early ? launch_tc_one<KK, VK, HD_, NT_, NG_, PT, false, true>(t, lc)                \
-                     : launch_tc_one<KK, VK, HD_, NT_, NG_, PT, false, false>(t, lc);              \
+      return launch_tc_mode<KK, VK, HD_, NT_, NG_, PT, false>(t, lc);                              \
     }
   KVQ_TC(64, 1, 1)
   KVQ_TC(64, 1, 2)

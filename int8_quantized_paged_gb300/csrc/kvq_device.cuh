@@ -50,6 +50,13 @@ __device__ __forceinline__ void store_param(uint8_t* p, int param, float v) {
   }
 }
 
+// Row of token t >= 0 among its sequence's pages: t in an append-only table
+// (ring_rows 0); else the first pin_rows rows are pinned and the rest a ring.
+__device__ __forceinline__ int row_of(int t, int ring_rows, int pin_rows) {
+  if (ring_rows == 0 || t < pin_rows) return t;
+  return pin_rows + (t - pin_rows) % ring_rows;
+}
+
 __device__ __forceinline__ void report(int32_t* status, int bits) {
   if (status) atomicOr(status, bits);
 }
@@ -98,6 +105,33 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* w) {
   } else {
     static_assert(NB == 2, "NB");
     w[0] = __ldg(reinterpret_cast<const unsigned short*>(p));
+  }
+}
+
+// 16 stored elements of row `slot` of a page sub-block, from element 16 * u.
+template <int KIND>
+__device__ __forceinline__ void read16(const uint8_t* sub, const PoolLayout& L, int slot, int u, float (&x)[16]) {
+  constexpr int P = 16;
+  constexpr int NB = KIND == KVQ_F16_KV ? 32 : (KIND == KVQ_SYM_INT8 ? 16 : 8);
+  uint32_t w[NB / 4];
+  load_words<NB>(sub + slot * L.code_bytes + u * NB, w);
+  if constexpr (KIND == KVQ_F16_KV) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      x[j] = __half2float(__ushort_as_half((unsigned short)(w[j / 2] >> (16 * (j & 1)))));
+  } else {
+    constexpr bool AFF = KIND == KVQ_AFFINE_INT4;
+    const int g = 16 * u / L.group;
+    const uint8_t* p = sub + P * L.code_bytes + slot * L.param_row_bytes;
+    const int pb = param_bytes(L.param);
+    const float s = load_param(p + (AFF ? 2 * g : g) * pb, L.param);
+    const float b = AFF ? load_param(p + (2 * g + 1) * pb, L.param) : 0.f;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      // offset binary: the unsigned nibble minus 8
+      const float c = KIND == KVQ_SHIMMY_INT4 ? code_aff4(w[j >> 3], j & 7) - 8.0f : code_at<KIND>(w, j);
+      x[j] = AFF ? fmaf(s, c, b) : __fmul_rn(s, c);
+    }
   }
 }
 

@@ -126,6 +126,16 @@ PoolLayout pool_layout(const kvq_config& c, int which) {
   return L;
 }
 
+kvq_status check_layout(const kvq_config& c, int32_t max_pages_per_seq, int32_t ring_rows, int32_t sinks) {
+  if (sinks < 0) return fail(KVQ_ERR_INVALID_ARG, "sinks (%d) < 0", sinks);
+  const int64_t pinned = ring_rows > 0 ? ((int64_t)sinks + c.page_size - 1) / c.page_size : 0;
+  if (ring_rows < 0 || ring_rows % c.page_size != 0 || pinned + ring_rows / c.page_size > max_pages_per_seq)
+    return fail(KVQ_ERR_INVALID_ARG,
+                "ring_rows %d must be a multiple of page_size that fits the table (%d pages) beside the pinned pages",
+                ring_rows, max_pages_per_seq);
+  return KVQ_OK;
+}
+
 float score_scale_log2(const kvq_config& c) {
   const double alpha = c.attn_scale > 0.f ? (double)c.attn_scale : 1.0 / std::sqrt((double)c.head_dim);
   return (float)(alpha * 1.4426950408889634);  // log2(e)

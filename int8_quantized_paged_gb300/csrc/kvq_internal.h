@@ -54,6 +54,14 @@ size_t smem_per_sm();   // shared memory of one SM of the current device (bytes)
 // KVQ_PDL=0 in the environment to turn it off).
 bool pdl_enabled();
 
+// Rows pinned in front of a ring for `sinks` first tokens (whole pages); 0
+// without a ring, where every row stays.
+inline int32_t pinned_rows(const kvq_config& c, int32_t ring_rows, int32_t sinks) {
+  return ring_rows > 0 ? (int32_t)(((int64_t)sinks + c.page_size - 1) / c.page_size * c.page_size) : 0;
+}
+// Checks of ring_rows and sinks against the table's width.
+kvq_status check_layout(const kvq_config& c, int32_t max_pages_per_seq, int32_t ring_rows, int32_t sinks);
+
 // Number of chunks a sequence of up to max_tokens attended tokens is split into.
 int chunk_tokens_for(const kvq_config& c, int32_t batch, int64_t max_tokens,
                      int32_t requested);

@@ -19,7 +19,7 @@ LIB_PATH = os.path.join(_HERE, "libkvq.so")
 # Enumerations of kvq.h.
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_OUT_OF_PAGES, ERR_BAD_BLOCK_TABLE, \
     ERR_WORKSPACE_TOO_SMALL, ERR_CUDA = range(7)
-DEV_BAD_PAGE, DEV_BAD_POS, DEV_BAD_SEQ, DEV_BAD_LEN = 1, 2, 4, 8
+DEV_BAD_PAGE, DEV_BAD_POS, DEV_BAD_SEQ, DEV_BAD_LEN, DEV_TIMEOUT = 1, 2, 4, 8, 16
 F32, F16, BF16 = 0, 1, 2
 SYM_INT4, SYM_INT8, AFFINE_INT4, F16_KV, F32_KV, SHIMMY_INT4 = range(6)
 ROPE_NONE, ROPE_NORMAL, ROPE_NEOX = 0, 1, 2
@@ -95,6 +95,17 @@ _SIGS = {
                                     _i32, _vp, _vp, _sz, _i32, _vp, _vp]),
     "kvq_decode_attention_noalloc": (C.c_int, [_cfgp, _i32, _vp, _vp, _vp, _i32, _vp, _i32, _vp, _vp,
                                                _i32, _vp, _i32, _vp, _vp]),
+    "kvq_read": (C.c_int, [_cfgp, _i32, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _vp, _i32, _vp, _vp, _vp, _vp]),
+    "kvq_append_sink": (C.c_int, [_cfgp, _i32, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, _i32, _vp, _i32,
+                                  _vp, _vp, _i32, _vp, _vp]),
+    "kvq_sink_workspace_bytes": (_sz, [_cfgp, _i32, _i32, _i32, _i32, _i32, _i32]),
+    "kvq_sink_decode": (C.c_int, [_cfgp, _i32, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32, _vp, _vp,
+                                  _i32, _vp, _vp, _sz, _i32, _vp, _vp]),
+    "kvq_append_sink_decode": (C.c_int, [_cfgp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32,
+                                         _i32, _vp, _vp, _i32, _vp, _vp, _sz, _i32, _vp, _vp]),
+    "kvq_prefill_workspace_bytes": (_sz, [_cfgp, _i32, _i32, _i32, _i32, _i32, _i32]),
+    "kvq_prefill_attention": (C.c_int, [_cfgp, _i32, _i32, _vp, _vp, _vp, _vp, _i32, _vp, _i32, _i32, _i32, _i32,
+                                        _vp, _vp, _i32, _vp, _vp, _sz, _vp, _vp]),
     "kvq_clear_device_status": (C.c_int, [_vp, _vp]),
     "kvq_get_device_status": (C.c_int, [_vp, _vp, C.POINTER(_i32)]),
 }
@@ -363,6 +374,73 @@ def window_decode(cfg: Config, q, k_pool, v_pool, n_pool_pages: int, ring_table,
         C.byref(cfg), q.shape[0], _ptr(q), _ptr(k_pool), _ptr(v_pool), n_pool_pages, _ptr(ring_table),
         ring_rows, window, _ptr(seq_lens), _ptr(rope_tab), rope_max_pos, _ptr(out), _ptr(workspace),
         workspace.numel() * workspace.element_size(), chunk_tokens, _ptr(dev_status), _stream(stream)))
+
+
+def read(cfg: Config, seq_ids, pos, block_table, n_seqs: int, max_pages_per_seq: int, ring_rows: int, sinks: int,
+         k_pool, v_pool, n_pool_pages: int, k_out, v_out, dev_status, stream=None) -> None:
+    """Stored K and V rows of tokens pos[i] of sequences seq_ids[i] as numbers of the activation type."""
+    _check(lib().kvq_read(C.byref(cfg), pos.shape[0], _ptr(seq_ids), _ptr(pos), _ptr(block_table), n_seqs,
+                          max_pages_per_seq, ring_rows, sinks, _ptr(k_pool), _ptr(v_pool), n_pool_pages,
+                          _ptr(k_out), _ptr(v_out), _ptr(dev_status), _stream(stream)))
+
+
+def append_sink(cfg: Config, k_new, v_new, seq_ids, pos, block_table, n_seqs: int, max_pages_per_seq: int,
+                ring_rows: int, sinks: int, rope_tab, rope_max_pos: int, k_pool, v_pool, n_pool_pages: int,
+                dev_status, stream=None) -> None:
+    """kvq_append into a table whose first pages are pinned for `sinks` tokens in front of the ring."""
+    _check(lib().kvq_append_sink(C.byref(cfg), k_new.shape[0], _ptr(k_new), _ptr(v_new), _ptr(seq_ids), _ptr(pos),
+                                 _ptr(block_table), n_seqs, max_pages_per_seq, ring_rows, sinks, _ptr(rope_tab),
+                                 rope_max_pos, _ptr(k_pool), _ptr(v_pool), n_pool_pages, _ptr(dev_status),
+                                 _stream(stream)))
+
+
+def sink_workspace_bytes(cfg: Config, batch: int, max_pages_per_seq: int, ring_rows: int, sinks: int, window: int,
+                         chunk_tokens: int = 0) -> int:
+    n = lib().kvq_sink_workspace_bytes(C.byref(cfg), batch, max_pages_per_seq, ring_rows, sinks, window, chunk_tokens)
+    if n == 0:
+        raise KvqError(ERR_INVALID_ARG, last_error())
+    return n
+
+
+def sink_decode(cfg: Config, q, k_pool, v_pool, n_pool_pages: int, block_table, max_pages_per_seq: int,
+                ring_rows: int, sinks: int, window: int, seq_lens, rope_tab, rope_max_pos: int, out, workspace,
+                dev_status, chunk_tokens: int = 0, stream=None) -> None:
+    """Decode over the last `window` tokens and the first `sinks` ones."""
+    _check(lib().kvq_sink_decode(
+        C.byref(cfg), q.shape[0], _ptr(q), _ptr(k_pool), _ptr(v_pool), n_pool_pages, _ptr(block_table),
+        max_pages_per_seq, ring_rows, sinks, window, _ptr(seq_lens), _ptr(rope_tab), rope_max_pos, _ptr(out),
+        _ptr(workspace), workspace.numel() * workspace.element_size(), chunk_tokens, _ptr(dev_status),
+        _stream(stream)))
+
+
+def append_sink_decode(cfg: Config, q, k_new, v_new, pos, k_pool, v_pool, n_pool_pages: int, block_table,
+                       max_pages_per_seq: int, ring_rows: int, sinks: int, window: int, seq_lens, rope_tab,
+                       rope_max_pos: int, out, workspace, dev_status, chunk_tokens: int = 0, stream=None) -> None:
+    """kvq_append_sink of row b at pos[b] for every sequence b, then kvq_sink_decode, in one call."""
+    _check(lib().kvq_append_sink_decode(
+        C.byref(cfg), q.shape[0], _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(pos), _ptr(k_pool), _ptr(v_pool),
+        n_pool_pages, _ptr(block_table), max_pages_per_seq, ring_rows, sinks, window, _ptr(seq_lens), _ptr(rope_tab),
+        rope_max_pos, _ptr(out), _ptr(workspace), workspace.numel() * workspace.element_size(), chunk_tokens,
+        _ptr(dev_status), _stream(stream)))
+
+
+def prefill_workspace_bytes(cfg: Config, batch: int, n_rows: int, max_pages_per_seq: int, ring_rows: int = 0,
+                            sinks: int = 0, window: int = 0) -> int:
+    n = lib().kvq_prefill_workspace_bytes(C.byref(cfg), batch, n_rows, max_pages_per_seq, ring_rows, sinks, window)
+    if n == 0:
+        raise KvqError(ERR_INVALID_ARG, last_error())
+    return n
+
+
+def prefill_attention(cfg: Config, q, q_starts, k_pool, v_pool, n_pool_pages: int, block_table,
+                      max_pages_per_seq: int, ring_rows: int, sinks: int, window: int, seq_lens, rope_tab,
+                      rope_max_pos: int, out, workspace, dev_status, stream=None) -> None:
+    """Causal attention of the last tokens of every sequence (rows q_starts[b] .. q_starts[b+1] of q)."""
+    _check(lib().kvq_prefill_attention(
+        C.byref(cfg), q_starts.shape[0] - 1, q.shape[0], _ptr(q), _ptr(q_starts), _ptr(k_pool), _ptr(v_pool),
+        n_pool_pages, _ptr(block_table), max_pages_per_seq, ring_rows, sinks, window, _ptr(seq_lens),
+        _ptr(rope_tab), rope_max_pos, _ptr(out), _ptr(workspace), workspace.numel() * workspace.element_size(),
+        _ptr(dev_status), _stream(stream)))
 
 
 def clear_device_status(dev_status, stream=None) -> None:
