@@ -10,6 +10,7 @@
 #include <cuda_runtime.h>
 
 #include "kvq_prefill.cuh"
+#include "kvq_prefill_tc.h"
 
 namespace kvq {
 
@@ -258,12 +259,19 @@ struct PrefillPlan {
 // longest range the table allows.
 constexpr int kMinSplitKeys = 256;
 
+// Whether the tensor-core kernel takes this config: 16-bit activations (its
+// operands are fp16) and scale groups of whole 32-dim units.
+static bool prefill_tc_takes(const kvq_config& c) {
+  if (c.act_dtype == KVQ_F32) return false;
+  return c.k_dtype == KVQ_F16_KV || (c.k_group % 32 == 0 && c.v_group % 32 == 0);
+}
+
 static PrefillPlan make_prefill_plan(const kvq_config& c, int32_t batch, int32_t n_rows, int32_t max_pages,
                                      int32_t sinks, int32_t window) {
   PrefillPlan p{};
   const int G = c.n_heads / c.n_kv_heads;
-  p.tc = false;
-  p.tq = kSimtRows / G;
+  p.tc = prefill_tc_takes(c);
+  p.tq = (p.tc ? prefill_tc_rows(c.head_dim) : kSimtRows) / G;
   const int64_t tiles = (int64_t)n_rows / p.tq + batch;
   p.n_tiles = (int)(tiles > INT_MAX ? INT_MAX : tiles);
   int64_t keys = (int64_t)max_pages * c.page_size;
@@ -375,10 +383,17 @@ extern "C" kvq_status kvq_prefill_attention(const kvq_config* cfg, int32_t batch
   lc.attrs = at;
   lc.numAttrs = pdl_enabled() ? 1 : 0;
   cudaError_t e;
-  switch (cfg->head_dim) {
-    case 64: e = launch_simt<64>(lc, a); break;
-    case 128: e = launch_simt<128>(lc, a); break;
-    default: e = launch_simt<256>(lc, a); break;
+  if (p.tc) {
+    const int64_t blocks = (int64_t)p.n_tiles * cfg->n_kv_heads * p.n_splits;
+    if (blocks > INT_MAX) return fail(KVQ_ERR_INVALID_ARG, "too many rows");
+    lc.gridDim = dim3((unsigned)blocks);
+    e = launch_prefill_tc(lc, cfg->head_dim, a);
+  } else {
+    switch (cfg->head_dim) {
+      case 64: e = launch_simt<64>(lc, a); break;
+      case 128: e = launch_simt<128>(lc, a); break;
+      default: e = launch_simt<256>(lc, a); break;
+    }
   }
   if (e == cudaSuccess && p.n_splits > 1) {
     lc.gridDim = dim3((unsigned)p.n_tiles, (unsigned)cfg->n_kv_heads, 8);

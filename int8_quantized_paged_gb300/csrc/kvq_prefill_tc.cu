@@ -1,0 +1,791 @@
+// Prefill attention on the fifth-generation tensor cores (tcgen05), for f16
+// and bf16 activations.
+//
+// A CTA takes MT tiles of 128 query rows (a row is a query token and one of
+// the G heads that share the kv head) over the keys they attend, 128 keys a
+// step:
+//   S = Q' K'^T   (fp16 operands in shared memory, fp32 in tensor memory)
+//   P = 2^(S f - m + 7), rounded to fp16 and written back over S
+//   O += P V'     (P from tensor memory, V' from shared memory)
+// Roles, by warp: MT warpgroups of softmax (a thread owns a row: no shuffles),
+// one warpgroup that dequantizes K and one that dequantizes V (a thread owns a
+// key), and a warp whose first lane issues the products.  They meet at
+// mbarriers only.  With two row tiles the products of one run while the other's
+// softmax does; head_dim 256 has room for one row tile in tensor memory, so its
+// S is double-buffered instead.
+//
+// K' and V' sit in shared memory as blocks of 128 keys x 64 dims in the
+// 128-byte swizzle, in two rings of four blocks.  Codes become exact fp16
+// integers by a mantissa trick, two nibbles of a word at a time, so the dims of
+// every eight are stored in the order 0 4 1 5 2 6 3 7 (4-bit) or, of every
+// four, 0 2 1 3 (8-bit); Q' is stored in the same order and the output is put
+// back in order when it is written.
+//
+// fp16 range.  Operands are fp16 for every activation type: its 11 bits cost a
+// bf16 result nothing, where bf16's 8 would add as much error as the result's
+// own rounding.  A query row, the 128 keys of a step and the values seen so far
+// are each held at a power-of-two scale (chosen from the row's largest element,
+// and from the scales of the step's keys) that puts the largest magnitude in
+// [2^14, 2^15): exact, and free, as the factors go into f, the one multiplier of
+// a row's scores in a step, and into the last scaling of O.  When a step's
+// values are larger than all before, O is rescaled, as it is when the running
+// maximum rises by more than 2^8; P is held times 2^7, which keeps weights down
+// to 2^-21 of the largest in fp16's normal range.
+//
+// Keys that no row may see (behind the last token, bad pages) are zero rows
+// and masked; a key whose scale or element is not finite is a zero row and a
+// bit that turns the scores of the rows that attend it into NaN, so it spoils
+// no other row of the tile.
+//
+// Every wait is bounded (two seconds): when one runs out the CTA runs through
+// its remaining steps without waiting, frees its tensor memory and reports
+// KVQ_DEV_TIMEOUT.
+#include <cuda_runtime.h>
+
+#include "kvq_prefill.cuh"
+#include "kvq_prefill_tc.h"
+#include "kvq_umma_ptx.cuh"
+
+namespace kvq {
+namespace {
+
+using namespace um;
+
+constexpr int kKeys = 128;               // keys a step
+constexpr int kStages = 4;               // blocks of a ring
+constexpr int kBlockBytes = kKeys * 128; // 128 keys x 64 dims of fp16
+constexpr int kSlots = 8;                // steps whose metadata are kept
+constexpr float kLazy = 8.0f;            // the running maximum rises past +2^8 only
+constexpr float kShift = 7.0f;           // P is held times 2^7
+
+__host__ __device__ constexpr int row_tiles(int hd) { return hd == 256 ? 1 : 2; }
+__host__ __device__ constexpr int tc_threads(int hd) { return 128 * row_tiles(hd) + 256 + 32; }
+
+// What the softmax needs to know about a step's keys.
+struct StepMeta {
+  uint32_t skip[4];   // keys left out (bad pages), a bit each
+  uint32_t bad[4];    // keys that are not finite
+  int e;              // the exponent they are held at
+  int pad[3];
+};
+
+template <int HD>
+struct Shared {
+  static constexpr int MT = row_tiles(HD);
+  static constexpr int HB = HD / 64;
+  uint8_t q[MT * HB * kBlockBytes];
+  uint8_t k[kStages * kBlockBytes];
+  uint8_t v[kStages * kBlockBytes];
+  StepMeta km[kSlots], vm[kSlots];
+  float qscale[MT * 128];   // f without the keys' part
+  uint32_t red[2][2][4];
+  uint64_t kfull[kStages], kempty[kStages], vfull[kStages], vempty[kStages];
+  uint64_t vmeta[kSlots];
+  uint64_t qfull[2], sfull[2], pfull[2];
+  uint64_t ofull[2];   // O of a row tile: its last step (two row tiles), or every step (one)
+  uint64_t drain;
+  uint32_t tmem;
+  int stop;
+};
+template <int HD>
+constexpr size_t shared_bytes() { return sizeof(Shared<HD>) + 1024; }   // the blocks want 1024-byte alignment
+
+__device__ __forceinline__ float pow2i(int e) {   // 2^e, 0 below 2^-126
+  return e < -126 ? 0.f : __int_as_float((e + 127) << 23);
+}
+// The exponent that holds magnitudes up to x (finite, >= 0) in [2^14, 2^15),
+// as far as both factors stay normal floats.
+__device__ __forceinline__ int hold_exponent(float x) {
+  const int e = (int)(__float_as_uint(x) >> 23) - 127 - 14;
+  return min(max(e, -100), 112);
+}
+__device__ __forceinline__ void group_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+
+__device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+__device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
+
+// How the dims of every eight are ordered in shared memory (see above).
+__host__ __device__ constexpr int order_of(int kind) {
+  return kind == KVQ_F16_KV ? 0 : (kind == KVQ_SYM_INT8 ? 1 : 2);
+}
+// The dim (0..7) at position i of an ordered group of eight.
+__host__ __device__ constexpr int dim_at(int order, int i) {
+  return order == 0 ? i : (order == 1 ? (i & 4) | ((i & 1) << 1) | ((i >> 1) & 1) : (i >> 1) | ((i & 1) << 2));
+}
+// The position of dim d of eight.
+__host__ __device__ constexpr int pos_of(int order, int d) {
+  return order == 0 ? d : (order == 1 ? (d & 4) | ((d & 1) << 1) | ((d >> 1) & 1) : ((d & 3) << 1) | (d >> 2));
+}
+
+// Eight codes (one word; two words for 8-bit kinds) to eight fp16 values
+// s * code (+ b), in order_of(KIND).
+template <int KIND>
+__device__ __forceinline__ uint4 dequant8(uint32_t w0, uint32_t w1, __half2 s, __half2 b) {
+  uint32_t r[4];
+  if constexpr (KIND == KVQ_SYM_INT8) {
+    const __half2 off = u2h(0x64806480u);   // 1024 + 128
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t w = i ? w1 : w0;
+      r[2 * i] = h2u(__hmul2(__hsub2(u2h((w & 0x00FF00FFu) ^ 0x64806480u), off), s));
+      r[2 * i + 1] = h2u(__hmul2(__hsub2(u2h(((w >> 8) & 0x00FF00FFu) ^ 0x64806480u), off), s));
+    }
+  } else {
+    constexpr bool SYM = KIND == KVQ_SYM_INT4, AFF = KIND == KVQ_AFFINE_INT4;
+    // low nibble of a byte: 1024 + n; high nibble: 1024 + 16 n, brought back by
+    // an exact fused multiply-add; n = code + 8 but for affine codes
+    constexpr uint32_t ml = SYM ? 0x64086408u : 0x64006400u, mh = SYM ? 0x64806480u : 0x64006400u;
+    const __half2 lo = u2h(AFF ? 0x64006400u : 0x64086408u);               // 1024 (+ 8)
+    const __half2 hi = AFF ? __floats2half2_rn(-64.f, -64.f) : __floats2half2_rn(-72.f, -72.f);
+    const __half2 six = __floats2half2_rn(0.0625f, 0.0625f);
+    const uint32_t w1s = w0 >> 8;
+    __half2 c[4];
+    c[0] = __hsub2(u2h((w0 & 0x000F000Fu) ^ ml), lo);
+    c[1] = __hfma2(u2h((w0 & 0x00F000F0u) ^ mh), six, hi);
+    c[2] = __hsub2(u2h((w1s & 0x000F000Fu) ^ ml), lo);
+    c[3] = __hfma2(u2h((w1s & 0x00F000F0u) ^ mh), six, hi);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = h2u(AFF ? __hfma2(c[i], s, b) : __hmul2(c[i], s));
+  }
+  return make_uint4(r[0], r[1], r[2], r[3]);
+}
+
+// The dequantizing warpgroup of K or V: thread pt owns key pt of every step.
+template <int KIND, int HD, bool IS_V>
+__device__ void produce(const PrefillArgs& a, const PrefillTile& t, const KeyRange& kr, int j0, int n, int kvh, int pt,
+                        Shared<HD>& sh, volatile int* stop) {
+  constexpr int P = 16, HB = HD / 64;
+  constexpr bool F16 = KIND == KVQ_F16_KV, AFF = KIND == KVQ_AFFINE_INT4;
+  constexpr int ROWB = F16 ? 2 * HD : (KIND == KVQ_SYM_INT8 ? HD : HD / 2);   // bytes of a row's codes
+  constexpr int NP = ROWB <= 128 ? 1 : HB;    // a row is loaded in NP pieces
+  constexpr int PB = HB / NP;                 // blocks a piece
+  constexpr int BW = ROWB / HB / 4;           // words a block
+  constexpr int NU = HD / 32;                 // 32-dim units: groups are 32 dims or more
+  const PoolLayout& L = IS_V ? a.vl : a.kl;
+  const uint8_t* pool = (IS_V ? a.v_pool : a.k_pool) + (int64_t)kvh * L.sub_bytes;
+  const int32_t* bt = a.block_table + (int64_t)t.b * a.max_pages;
+  const int warp = pt >> 5, lane = pt & 31;
+  const uint32_t ring = smem_u32(IS_V ? sh.v : sh.k);
+  uint64_t* full = IS_V ? sh.vfull : sh.kfull;
+  uint64_t* empty = IS_V ? sh.vempty : sh.kempty;
+  const int pb = param_bytes(L.param);
+  const int gu = F16 ? NU : L.group / 32;     // units a group
+
+  // row of key pt in step i, -1 behind the end; its page id
+  auto row_at = [&](int i) {
+    const int key = kr.base<kKeys>(j0 + i) + pt;
+    return i < n && key < kr.end(j0 + i) ? row_of(key, a.ring_rows, a.pin_rows) : -1;
+  };
+  uint32_t raw[PB * BW];
+  float sc[F16 ? 1 : NU], bi[AFF ? NU : 1];
+  const uint8_t* src = nullptr;   // the row's codes, null when there is no such row
+  auto load_piece = [&](int p) {
+#pragma unroll
+    for (int i = 0; i < PB * BW / 4; ++i) {
+      const uint4 x = src ? __ldg(reinterpret_cast<const uint4*>(src + p * (PB * BW * 4)) + i) : make_uint4(0, 0, 0, 0);
+      raw[4 * i] = x.x;
+      raw[4 * i + 1] = x.y;
+      raw[4 * i + 2] = x.z;
+      raw[4 * i + 3] = x.w;
+    }
+  };
+  bool skip = false;
+  auto load_row = [&](int row, int page) {
+    skip = false;
+    src = nullptr;
+    const uint8_t* par = nullptr;
+    if (row >= 0) {
+      if (page < 0 || page >= a.n_pool_pages) {
+        skip = true;
+        report(a.status, KVQ_DEV_BAD_PAGE);
+      } else {
+        const uint8_t* sub = pool + page * L.page_bytes;
+        src = sub + (row % P) * L.code_bytes;
+        par = sub + P * L.code_bytes + (row % P) * L.param_row_bytes;
+      }
+    }
+    load_piece(0);
+    if constexpr (!F16) {
+#pragma unroll
+      for (int u = 0; u < NU; ++u) {
+        if (u % gu == 0) {
+          const int g = u / gu;
+          sc[u] = par ? load_param(par + (AFF ? 2 * g : g) * pb, L.param) : 0.f;
+          if constexpr (AFF) bi[u] = par ? load_param(par + (2 * g + 1) * pb, L.param) : 0.f;
+        } else {
+          sc[u] = sc[u - (u > 0)];
+          if constexpr (AFF) bi[u] = bi[u - (u > 0)];
+        }
+      }
+    }
+  };
+
+  int held = IS_V ? -100 : 0;   // V: the exponent held so far
+  int row = row_at(0);
+  load_row(row, row >= 0 ? bt[row / P] : -1);
+  for (int i = 0; i < n; ++i) {
+    const int row_next = row_at(i + 1);
+    const int page_next = row_next >= 0 ? bt[row_next / P] : -1;
+    StepMeta& meta = (IS_V ? sh.vm : sh.km)[i % kSlots];
+    bool bad = false;
+    float down = 1.f;
+    if constexpr (!F16) {
+      // the largest magnitude of the step's values
+      float amp = 0.f;
+#pragma unroll
+      for (int u = 0; u < NU; ++u) {
+        float x;
+        if constexpr (AFF) x = fmaxf(fabsf(bi[u]), fabsf(fmaf(15.f, sc[u], bi[u])));
+        else x = fabsf(sc[u]) * (KIND == KVQ_SYM_INT8 ? 127.f : 8.f);
+        bad |= !(x <= 3.0e38f) || !isfinite(sc[u]);
+        amp = fmaxf(amp, x);
+      }
+      if (bad) amp = 0.f;
+      const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(amp));
+      if (lane == 0) sh.red[IS_V][i & 1][warp] = top;
+      group_sync(IS_V ? 2 : 1);
+      const uint32_t* r = sh.red[IS_V][i & 1];
+      const int e = hold_exponent(__uint_as_float(max(max(r[0], r[1]), max(r[2], r[3]))));
+      held = IS_V ? max(held, e) : e;
+      down = pow2i(-held);
+    } else {
+      held = 0;
+    }
+    const bool gone = bad || src == nullptr;
+    if (!F16 || !IS_V) {
+      const uint32_t ws = __ballot_sync(0xffffffffu, skip), wb = __ballot_sync(0xffffffffu, bad);
+      if (lane == 0) {
+        meta.skip[warp] = ws;
+        meta.bad[warp] = wb;
+        if (warp == 0) meta.e = held;
+        if (IS_V) mbar_arrive(smem_u32(&sh.vmeta[i % kSlots]));
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < HB; ++h) {
+      const int c = i * HB + h, st = c % kStages;
+      mbar_wait(smem_u32(&empty[st]), (c / kStages + 1) & 1, stop);
+      const uint32_t dst = ring + st * kBlockBytes + pt * 128;
+      const uint32_t* w = raw + (h % PB) * BW;
+      if constexpr (F16) {
+        uint32_t inf = 0;   // a half with all exponent bits set carries into its sign bit
+#pragma unroll
+        for (int x = 0; x < BW; ++x) inf |= ((w[x] & 0x7FFF7FFFu) + 0x04000400u) & 0x80008000u;
+        bad |= inf != 0;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          const uint32_t at = dst + ((x ^ (pt & 7)) << 4);
+          const bool z = inf != 0;
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(z ? 0u : w[4 * x]),
+                       "r"(z ? 0u : w[4 * x + 1]), "r"(z ? 0u : w[4 * x + 2]), "r"(z ? 0u : w[4 * x + 3])
+                       : "memory");
+        }
+        if (h == HB - 1) {   // known only now
+          const uint32_t wb = __ballot_sync(0xffffffffu, bad);
+          if (lane == 0) {
+            meta.bad[warp] = wb;
+            if (IS_V) {
+              meta.skip[warp] = 0;
+              if (warp == 0) meta.e = 0;
+              mbar_arrive(smem_u32(&sh.vmeta[i % kSlots]));
+            }
+          }
+        }
+      } else {
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          const int u = (64 * h + 8 * x) / 32;
+          const float s = gone ? 0.f : sc[u] * down, b = AFF && !gone ? bi[AFF ? u : 0] * down : 0.f;
+          uint4 y;
+          if constexpr (KIND == KVQ_SYM_INT8)
+            y = dequant8<KIND>(w[2 * x], w[2 * x + 1], __float2half2_rn(s), __float2half2_rn(b));
+          else
+            y = dequant8<KIND>(w[x], 0, __float2half2_rn(s), __float2half2_rn(b));
+          const uint32_t at = dst + ((x ^ (pt & 7)) << 4);
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w)
+                       : "memory");
+        }
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&full[st]));
+      // the next loads are in flight while this warpgroup waits for a free block
+      if (h == HB - 1) load_row(row_next, page_next);
+      else if ((h + 1) % PB == 0) load_piece((h + 1) / PB);
+    }
+  }
+}
+
+template <int HD, bool IS_V>
+__device__ __forceinline__ void produce_kind(int kind, const PrefillArgs& a, const PrefillTile& t, const KeyRange& kr,
+                                             int j0, int n, int kvh, int pt, Shared<HD>& sh, volatile int* stop) {
+  switch (kind) {
+    case KVQ_SYM_INT4: return produce<KVQ_SYM_INT4, HD, IS_V>(a, t, kr, j0, n, kvh, pt, sh, stop);
+    case KVQ_SYM_INT8: return produce<KVQ_SYM_INT8, HD, IS_V>(a, t, kr, j0, n, kvh, pt, sh, stop);
+    case KVQ_AFFINE_INT4: return produce<KVQ_AFFINE_INT4, HD, IS_V>(a, t, kr, j0, n, kvh, pt, sh, stop);
+    case KVQ_SHIMMY_INT4: return produce<KVQ_SHIMMY_INT4, HD, IS_V>(a, t, kr, j0, n, kvh, pt, sh, stop);
+    default:
+      if constexpr (HD <= 128) return produce<KVQ_F16_KV, HD, IS_V>(a, t, kr, j0, n, kvh, pt, sh, stop);
+  }
+}
+
+// The queries of row tile rt, rotated, scaled into fp16 and stored as blocks
+// of 64 dims; HD / 8 lanes share a row.
+template <int HD>
+__device__ void load_queries(const PrefillArgs& a, const PrefillTile& t, int rows, int G, int kvh, int rt, int warp,
+                             int lane, Shared<HD>& sh) {
+  constexpr int HB = HD / 64, LANES = HD / 8, RPW = 32 / LANES;
+  const int li = lane % LANES;
+  const bool neox = a.rope == KVQ_ROPE_NEOX;
+  const int order = order_of(a.kl.kind);
+  const uint32_t base = smem_u32(sh.q) + rt * HB * kBlockBytes;
+  const int d0 = neox ? 4 * li : 8 * li, d1 = neox ? HD / 2 + 4 * li : 8 * li + 4;   // two runs of four
+#pragma unroll 4
+  for (int it = 0; it < 32 / RPW; ++it) {
+    const int r = warp * 32 + it * RPW + lane / LANES, R = rt * 128 + r;
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = 0.f;
+    if (R < rows) {
+      const int64_t at = ((int64_t)(t.row0 + R / G) * a.n_heads + kvh * G + R % G) * HD;
+      const unsigned short* q = static_cast<const unsigned short*>(a.q) + at;
+      const uint2 u0 = *reinterpret_cast<const uint2*>(q + d0), u1 = *reinterpret_cast<const uint2*>(q + d1);
+      const uint32_t u[4] = {u0.x, u0.y, u1.x, u1.y};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (a.act == KVQ_F16) {
+          const float2 f = __half22float2(u2h(u[i]));
+          x[2 * i] = f.x;
+          x[2 * i + 1] = f.y;
+        } else {
+          x[2 * i] = __uint_as_float(u[i] << 16);
+          x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+        }
+      }
+      if (a.rope != KVQ_ROPE_NONE) {   // both pairings meet pairs 4 li .. 4 li + 3
+        const float4* cs = reinterpret_cast<const float4*>(a.rope_tab + ((int64_t)(t.p0 + R / G) * (HD / 2) + 4 * li) * 2);
+        const float4 c0 = cs[0], c1 = cs[1];
+        const float c[4] = {c0.x, c0.z, c1.x, c1.z}, s[4] = {c0.y, c0.w, c1.y, c1.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float p = neox ? x[i] : x[2 * i], m = neox ? x[4 + i] : x[2 * i + 1];
+          const float y0 = p * c[i] - m * s[i], y1 = p * s[i] + m * c[i];
+          if (neox) {
+            x[i] = y0;
+            x[4 + i] = y1;
+          } else {
+            x[2 * i] = y0;
+            x[2 * i + 1] = y1;
+          }
+        }
+      }
+    }
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));
+#pragma unroll
+    for (int o = LANES / 2; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const int e = hold_exponent(top);
+    const float down = pow2i(-e);
+    if (li == 0) sh.qscale[R] = a.score_scale * pow2i(e);
+    __half y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = __float2half_rn(x[i] * down);
+    auto word = [&](int i, int j) {
+      return (uint32_t)__half_as_ushort(y[i]) | (uint32_t)__half_as_ushort(y[j]) << 16;
+    };
+    auto chunk = [&](int d) {   // address of the 16-byte chunk of dim d
+      return base + (d / 64) * kBlockBytes + r * 128 + (((d % 64 / 8) ^ (r & 7)) << 4);
+    };
+    if (!neox) {   // the lane's eight dims are one chunk
+      uint32_t w[4];
+      if (order == 2) {
+        w[0] = word(0, 4), w[1] = word(1, 5), w[2] = word(2, 6), w[3] = word(3, 7);
+      } else if (order == 1) {
+        w[0] = word(0, 2), w[1] = word(1, 3), w[2] = word(4, 6), w[3] = word(5, 7);
+      } else {
+        w[0] = word(0, 1), w[1] = word(2, 3), w[2] = word(4, 5), w[3] = word(6, 7);
+      }
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(chunk(d0)), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                   "r"(w[3])
+                   : "memory");
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int d = (i < 4 ? d0 : d1) + i % 4;
+        asm volatile("st.shared.b16 [%0], %1;" ::"r"(chunk(d) + 2 * pos_of(order, d & 7)), "h"(__half_as_ushort(y[i]))
+                     : "memory");
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Which of a step's 128 keys a row sees, and which of those are not finite.
+struct RowMask {
+  int hi, lo, sinks;   // columns c < hi with c >= lo or c < sinks
+  const uint32_t *skip, *kbad, *vbad;
+  __device__ __forceinline__ uint32_t visible(int c) const {   // columns 32 c .. 32 c + 31
+    auto below = [&](int x) -> uint32_t {   // bits of columns < x
+      const int k = min(max(x - 32 * c, 0), 32);
+      return k == 32 ? ~0u : (1u << k) - 1u;
+    };
+    return below(hi) & (~below(lo) | below(sinks)) & ~skip[c];
+  }
+  __device__ __forceinline__ void apply(int c, float (&x)[32]) const {
+    const uint32_t v = visible(c), b = v & (kbad[c] | vbad[c]);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = (b >> i) & 1u ? NAN : ((v >> i) & 1u ? x[i] : -INFINITY);
+  }
+};
+
+template <int HD>
+__global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __grid_constant__ PrefillArgs a) {
+  constexpr int MT = row_tiles(HD), HB = HD / 64;
+  constexpr int PVN = HD == 256 ? 64 : HD;        // output columns of one product
+  constexpr uint32_t kTmemCols = 512;
+  extern __shared__ uint8_t raw_smem[];
+  Shared<HD>& sh = *reinterpret_cast<Shared<HD>*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~(uintptr_t)1023);
+  volatile int* stop = &sh.stop;
+
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // block index: kv head fastest, then the split, then the tile, last tiles (the longest key ranges) first
+  const int kvh = blockIdx.x % a.n_kv_heads, rest = blockIdx.x / a.n_kv_heads;
+  const int split = rest % a.n_splits, x = a.n_tiles - 1 - rest / a.n_splits;
+  const int G = a.n_heads / a.n_kv_heads;
+  if (blockIdx.x == 0) check_starts(a, tid, tc_threads(HD));
+  PrefillTile t;
+  if (!find_tile(a, x, kvh == 0 && split == 0 && tid == 0, &t)) return;
+  const int rows = t.cnt * G;
+  auto out_row = [&](int r) -> int64_t { return (int64_t)(t.row0 + r / G) * a.n_heads + kvh * G + r % G; };
+  const int64_t ws0 = (int64_t)split * a.n_rows * a.n_heads;
+  KeyRange kr = key_range<kKeys>(a, t);
+  const int j0 = (int)((int64_t)split * kr.n / a.n_splits), j1 = (int)((int64_t)(split + 1) * kr.n / a.n_splits);
+  if (t.zero || j0 == j1) {   // no keys: zero rows, or an empty part
+    if (t.zero && split == 0) {
+      unsigned short* o = static_cast<unsigned short*>(a.out);
+      for (int i = tid; i < rows * HD; i += tc_threads(HD)) o[out_row(i / HD) * HD + i % HD] = 0;
+    }
+    if (a.n_splits > 1)
+      for (int r = tid; r < rows; r += tc_threads(HD)) a.ws_ml[ws0 + out_row(r)] = make_float2(-INFINITY, 0.f);
+    return;
+  }
+  const int n = j1 - j0;
+  const int na = MT == 1 || rows <= 128 ? 1 : 2;   // row tiles with rows
+  // Steps of row tile rt: the last ones may lie behind all of its queries.
+  auto last_pos = [&](int rt) { return t.p0 + (min(rows, rt * 128 + 128) - 1) / G; };
+  auto steps = [&](int rt) {
+    int k = n;
+    while (k > 0 && kr.base<kKeys>(j0 + k - 1) > last_pos(rt)) --k;
+    return k;
+  };
+
+  constexpr int kMmaWarp = 4 * MT + 8;
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(&sh.tmem), kTmemCols);
+  } else if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(smem_u32(&sh.kfull[i]), 4);
+      mbar_init(smem_u32(&sh.vfull[i]), 4);
+      mbar_init(smem_u32(&sh.kempty[i]), 1);
+      mbar_init(smem_u32(&sh.vempty[i]), 1);
+    }
+    for (int i = 0; i < kSlots; ++i) mbar_init(smem_u32(&sh.vmeta[i]), 4);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&sh.qfull[i]), 4);
+      mbar_init(smem_u32(&sh.sfull[i]), 1);
+      mbar_init(smem_u32(&sh.pfull[i]), 4);
+      mbar_init(smem_u32(&sh.ofull[i]), 1);
+    }
+    mbar_init(smem_u32(&sh.drain), 1);
+    sh.stop = 0;
+    mbar_init_fence();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  const uint32_t s_col = HD == 256 ? 256 : 0, o_col = HD == 256 ? 0 : 256;
+
+  if (warp < 4 * MT) {
+    // ------------------------------------------------------------ softmax
+    const int rt = warp >> 2;
+    if (rt < na) {
+      load_queries<HD>(a, t, rows, G, kvh, rt, warp & 3, lane, sh);
+      fence_async_smem();
+      group_sync(3 + rt);   // the row scales, written by other lanes
+      if (lane == 0) mbar_arrive(smem_u32(&sh.qfull[rt]));
+      const int R = rt * 128 + (tid & 127);
+      const int pos = t.p0 + min(R, rows - 1) / G;
+      const int pmin = t.p0 + rt * 128 / G, pmax = last_pos(rt);
+      const float qs = sh.qscale[R];
+      const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // this warp's 32 lanes of tensor memory
+      const uint32_t o_at = tmem + lanes + o_col + rt * HD;
+      const int nt = steps(rt);
+      float m = -INFINITY, l = 0.f;
+      int held = 0;
+      for (int i = 0; i < nt; ++i) {
+        const int buf = MT == 2 ? rt : i & 1;
+        const uint32_t s_at = tmem + lanes + s_col + buf * 128;
+        const StepMeta &km = sh.km[i % kSlots], &vm = sh.vm[i % kSlots];
+        mbar_wait(smem_u32(&sh.sfull[buf]), MT == 2 ? i & 1 : (i >> 1) & 1, stop);
+        mbar_wait(smem_u32(&sh.vmeta[i % kSlots]), (i / kSlots) & 1, stop);
+        tc_fence_after();
+        const float f = fmaxf(qs * pow2i(km.e), 1.17549435e-38f);   // never 0: -inf stays -inf
+        const int tb = kr.base<kKeys>(j0 + i), end = kr.end(j0 + i);
+        uint32_t odd = 0;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) odd |= km.skip[c] | km.bad[c] | vm.bad[c];
+        const bool whole = odd == 0 && tb + kKeys <= end && tb + kKeys - 1 <= pmin &&
+                           (a.window == 0 || tb > pmax - a.window || tb + kKeys <= a.sinks);
+        RowMask mask;
+        mask.hi = min(end - tb, pos - tb + 1);
+        mask.lo = a.window == 0 ? 0 : pos - a.window + 1 - tb;
+        mask.sinks = a.window == 0 ? 0 : a.sinks - tb;
+        mask.skip = km.skip;
+        mask.kbad = km.bad;
+        mask.vbad = vm.bad;
+
+        // the row's maximum; columns 64 .. 127 stay in registers
+        float x0[32], x1[32];
+        float mx = -INFINITY;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          tmem_ld32(s_at + 64 * half, x0);
+          tmem_ld32(s_at + 64 * half + 32, x1);
+          tmem_ld_wait(x0);
+          tmem_ld_wait(x1);
+          if (!whole) {
+            mask.apply(2 * half, x0);
+            mask.apply(2 * half + 1, x1);
+          }
+#pragma unroll
+          for (int c = 0; c < 32; ++c) mx = fmaxf(mx, fmaxf(x0[c], x1[c]));
+        }
+        mx *= f;
+        const bool raise = mx > m + kLazy;
+        const float mn = raise ? mx : m;
+        if (i == 0) {
+          m = mn;
+          held = vm.e;
+        } else if (__any_sync(0xffffffffu, raise || vm.e != held)) {
+          const float c = raise ? ex2(m - mn) : 1.f;   // 2^-inf = 0: no key so far
+          l *= c;
+          const float co = c * pow2i(held - vm.e);
+          m = mn;
+          held = vm.e;
+          // O is at rest: with two row tiles this step's scores were issued
+          // after the last step's O; with one, they were issued before it, but
+          // after that of the step before, so the parity is not ambiguous
+          if constexpr (MT == 1) {
+            mbar_wait(smem_u32(&sh.ofull[0]), (i - 1) & 1, stop);
+            tc_fence_after();
+          }
+#pragma unroll 1
+          for (int d = 0; d < HD; d += 32) {
+            float o[32];
+            tmem_ld32(o_at + d, o);
+            tmem_ld_wait(o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] *= co;
+            tmem_st32(o_at + d, o);
+          }
+        }
+        const float sub = m == -INFINITY ? 0.f : m - kShift;
+        // P over columns 64 .. 127 of S, 16 words for 32 keys
+        auto weights = [&](int c, const float (&x)[32]) {
+          uint32_t w[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float p0 = ex2(fmaf(x[2 * k], f, -sub)), p1 = ex2(fmaf(x[2 * k + 1], f, -sub));
+            l += p0 + p1;
+            w[k] = h2u(__floats2half2_rn(p0, p1));
+          }
+          tmem_st16(s_at + 64 + 16 * c, w);
+        };
+        weights(2, x0);
+        tmem_ld32(s_at, x0);
+        weights(3, x1);
+        tmem_ld32(s_at + 32, x1);
+        tmem_ld_wait(x0);
+        tmem_ld_wait(x1);
+        if (!whole) {
+          mask.apply(0, x0);
+          mask.apply(1, x1);
+        }
+        weights(0, x0);
+        weights(1, x1);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.pfull[buf]));
+      }
+      // ---- the result: O 2^held / l, dims back in order
+      if constexpr (MT == 1) {
+        if (nt > 1) mbar_wait(smem_u32(&sh.ofull[0]), (nt - 2) & 1, stop);
+        mbar_wait(smem_u32(&sh.ofull[0]), (nt - 1) & 1, stop);
+      } else if (nt > 0) {
+        mbar_wait(smem_u32(&sh.ofull[rt]), 0, stop);
+      }
+      tc_fence_after();
+      const bool mine = R < rows;
+      const int64_t orow = out_row(mine ? R : 0);
+      const float up = pow2i(held);
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const int order = order_of(a.vl.kind);
+      if (mine && a.n_splits > 1) a.ws_ml[ws0 + orow] = make_float2(m == -INFINITY ? m : m - kShift, l);
+#pragma unroll 1
+      for (int d = 0; d < HD; d += 32) {
+        float o[32], y[32];
+        if (nt > 0) {
+          tmem_ld32(o_at + d, o);
+          tmem_ld_wait(o);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] = 0.f;
+        }
+        if (order == 2) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) y[(e & ~7) | dim_at(2, e & 7)] = o[e];
+        } else if (order == 1) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) y[(e & ~7) | dim_at(1, e & 7)] = o[e];
+        } else {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) y[e] = o[e];
+        }
+        if (!mine) continue;
+        if (a.n_splits == 1) {
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float y0 = y[2 * e] * inv * up, y1 = y[2 * e + 1] * inv * up;
+            if (a.act == KVQ_F16) {
+              w[e] = h2u(__floats2half2_rn(y0, y1));
+            } else {
+              const __nv_bfloat162 h = __floats2bfloat162_rn(y0, y1);
+              w[e] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+          }
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<unsigned short*>(a.out) + orow * HD + d);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) dst[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+        } else {
+          float4* dst = reinterpret_cast<float4*>(a.ws_acc + (ws0 + orow) * HD + d);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            dst[e] = make_float4(y[4 * e] * up, y[4 * e + 1] * up, y[4 * e + 2] * up, y[4 * e + 3] * up);
+        }
+      }
+      tc_fence_before();
+    }
+  } else if (warp < 4 * MT + 4) {
+    produce_kind<HD, false>(a.kl.kind, a, t, kr, j0, n, kvh, tid - 128 * MT, sh, stop);
+  } else if (warp < kMmaWarp) {
+    produce_kind<HD, true>(a.vl.kind, a, t, kr, j0, n, kvh, tid - 128 * MT - 128, sh, stop);
+  } else {
+    // ------------------------------------------------------------ products
+    if (lane == 0) {
+    constexpr uint32_t id_qk = idesc_f16(kKeys, false), id_pv = idesc_f16(PVN, true);
+    const uint32_t qb = smem_u32(sh.q), kb = smem_u32(sh.k), vb = smem_u32(sh.v);
+    auto wait_full = [&](uint64_t* full, int c) {
+      mbar_wait(smem_u32(&full[c % kStages]), (c / kStages) & 1, stop);
+    };
+    const int nt0 = steps(0), nt1 = na == 2 ? steps(1) : 0;   // nt1 >= nt0: later queries
+    const int lt = na - 1;                                    // the row tile that uses a block last
+    // scores of row tile rt, step i
+    auto qk = [&](int rt, int i) {
+      const int buf = MT == 2 ? rt : i & 1;
+#pragma unroll 1
+      for (int h = 0; h < HB; ++h) {
+        const int c = i * HB + h;
+        wait_full(sh.kfull, c);
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          mma_ss(tmem + s_col + buf * 128, smem_desc(qb + (rt * HB + h) * kBlockBytes + 32 * k, 16),
+                 smem_desc(kb + (c % kStages) * kBlockBytes + 32 * k, 16), id_qk, h > 0 || k > 0);
+        if (rt == lt) mma_commit(smem_u32(&sh.kempty[c % kStages]));
+      }
+      mma_commit(smem_u32(&sh.sfull[buf]));
+    };
+    // O of row tile rt, step i
+    auto pv = [&](int rt, int i, int nt) {
+      const int buf = MT == 2 ? rt : i & 1;
+      mbar_wait(smem_u32(&sh.pfull[buf]), MT == 2 ? i & 1 : (i >> 1) & 1, stop);
+#pragma unroll 1
+      for (int h = 0; h < HB; h += PVN / 64) {
+        const int c = i * HB + h;
+#pragma unroll
+        for (int b = 0; b < PVN / 64; ++b) wait_full(sh.vfull, c + b);
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < kKeys / 16; ++k)
+          mma_ts(tmem + o_col + rt * HD + 64 * h, tmem + s_col + buf * 128 + 64 + 8 * k,
+                 smem_desc(vb + (c % kStages) * kBlockBytes + 2048 * k, kBlockBytes), id_pv, i > 0 || k > 0);
+        if (rt == lt) {
+#pragma unroll
+          for (int b = 0; b < PVN / 64; ++b) mma_commit(smem_u32(&sh.vempty[(c + b) % kStages]));
+        }
+      }
+      if (MT == 1 || i == nt - 1) mma_commit(smem_u32(&sh.ofull[rt]));
+    };
+    for (int rt = 0; rt < na; ++rt) {
+      mbar_wait(smem_u32(&sh.qfull[rt]), 0, stop);
+      if (0 < (rt ? nt1 : nt0)) qk(rt, 0);
+    }
+    for (int i = 0; i < n; ++i) {
+      if constexpr (MT == 1) {
+        if (i + 1 < n) qk(0, i + 1);
+        pv(0, i, n);
+      } else {
+#pragma unroll 1
+        for (int rt = 0; rt < na; ++rt) {
+          const int nt = rt ? nt1 : nt0;
+          if (i < nt) pv(rt, i, nt);
+          if (i + 1 < nt) qk(rt, i + 1);
+        }
+      }
+    }
+    mma_commit(smem_u32(&sh.drain));
+    mbar_wait(smem_u32(&sh.drain), 0, stop);
+    tc_fence_before();
+    }
+    __syncwarp();
+  }
+  __syncthreads();
+  if (tid == 0 && sh.stop) report(a.status, KVQ_DEV_TIMEOUT);
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int HD>
+cudaError_t launch(cudaLaunchConfig_t& lc, const PrefillArgs& a) {
+  lc.blockDim = dim3(tc_threads(HD));
+  lc.dynamicSmemBytes = shared_bytes<HD>();
+  const cudaError_t e = cudaFuncSetAttribute(prefill_tc_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)shared_bytes<HD>());
+  return e != cudaSuccess ? e : cudaLaunchKernelEx(&lc, prefill_tc_kernel<HD>, a);
+}
+
+}  // namespace
+
+int prefill_tc_rows(int head_dim) { return 128 * row_tiles(head_dim); }
+
+cudaError_t launch_prefill_tc(cudaLaunchConfig_t& lc, int head_dim, const PrefillArgs& a) {
+  switch (head_dim) {
+    case 64: return launch<64>(lc, a);
+    case 128: return launch<128>(lc, a);
+    default: return launch<256>(lc, a);
+  }
+}
+
+}  // namespace kvq
