@@ -5,7 +5,7 @@
 // the G heads that share the kv head) over the keys they attend, 128 keys a
 // step:
 //   S = Q' K'^T   (fp16 operands in shared memory, fp32 in tensor memory)
-//   P = 2^(S f - m + 7), rounded to fp16 and written back over S
+//   P = 2^(S f - m + 7), rounded to fp16 and written back over S, in one pass
 //   O += P V'     (P from tensor memory, V' from shared memory)
 // Roles, by warp: MT warpgroups of softmax (a thread owns a row: no shuffles),
 // one warpgroup that dequantizes K and one that dequantizes V (a thread owns a
@@ -80,7 +80,7 @@ struct Shared {
   float qscale[MT * 128];   // f without the keys' part
   uint32_t red[2][2][4];
   uint64_t kfull[kStages], kempty[kStages], vfull[kStages], vempty[kStages];
-  uint64_t vmeta[kSlots];
+  uint64_t kmeta[kSlots], vmeta[kSlots];   // a step's metadata are there
   uint64_t qfull[2], sfull[2], pfull[2];
   uint64_t ofull[2];   // O of a row tile: its last step (two row tiles), or every step (one)
   uint64_t drain;
@@ -151,168 +151,169 @@ __device__ __forceinline__ uint4 dequant8(uint32_t w0, uint32_t w1, __half2 s, _
 }
 
 // The dequantizing warpgroup of K or V: thread pt owns key pt of every step.
+// Loads run ahead of their use: a step's page id two steps, its parameters one
+// step, and its codes one piece (16 words of a row, two blocks of 4-bit codes).
 template <int KIND, int HD, bool IS_V>
 __device__ void produce(const PrefillArgs& a, const PrefillTile& t, const KeyRange& kr, int j0, int n, int kvh, int pt,
                         Shared<HD>& sh, volatile int* stop) {
   constexpr int P = 16, HB = HD / 64;
   constexpr bool F16 = KIND == KVQ_F16_KV, AFF = KIND == KVQ_AFFINE_INT4;
-  constexpr int ROWB = F16 ? 2 * HD : (KIND == KVQ_SYM_INT8 ? HD : HD / 2);   // bytes of a row's codes
-  constexpr int NP = ROWB <= 128 ? 1 : HB;    // a row is loaded in NP pieces
-  constexpr int PB = HB / NP;                 // blocks a piece
-  constexpr int BW = ROWB / HB / 4;           // words a block
-  constexpr int NU = HD / 32;                 // 32-dim units: groups are 32 dims or more
+  constexpr int BW = F16 ? 32 : (KIND == KVQ_SYM_INT8 ? 16 : 8);   // words of a block's codes
+  constexpr int PB = BW == 8 && HB > 1 ? 2 : 1;                    // blocks a piece
+  constexpr int NP = HB / PB;                                      // pieces a row
+  constexpr int W = PB * BW;
+  constexpr int NU = F16 ? 1 : HD / 32;                            // 32-dim units: groups are 32 dims or more
   const PoolLayout& L = IS_V ? a.vl : a.kl;
   const uint8_t* pool = (IS_V ? a.v_pool : a.k_pool) + (int64_t)kvh * L.sub_bytes;
   const int32_t* bt = a.block_table + (int64_t)t.b * a.max_pages;
   const int warp = pt >> 5, lane = pt & 31;
-  const uint32_t ring = smem_u32(IS_V ? sh.v : sh.k);
+  const uint32_t ring = smem_u32(IS_V ? sh.v : sh.k) + pt * 128;
   uint64_t* full = IS_V ? sh.vfull : sh.kfull;
   uint64_t* empty = IS_V ? sh.vempty : sh.kempty;
+  uint64_t* ready = IS_V ? sh.vmeta : sh.kmeta;
   const int pb = param_bytes(L.param);
-  const int gu = F16 ? NU : L.group / 32;     // units a group
+  const int gu = F16 ? 1 : L.group / 32;     // units a group
 
-  // row of key pt in step i, -1 behind the end; its page id
-  auto row_at = [&](int i) {
+  // Row of key pt in step i (-1: none), and its page id (-1 too).
+  auto row_at = [&](int i) -> int {
+    if (i >= n) return -1;
     const int key = kr.base<kKeys>(j0 + i) + pt;
-    return i < n && key < kr.end(j0 + i) ? row_of(key, a.ring_rows, a.pin_rows) : -1;
+    return key < kr.end(j0 + i) ? row_of(key, a.ring_rows, a.pin_rows) : -1;
   };
-  uint32_t raw[PB * BW];
-  float sc[F16 ? 1 : NU], bi[AFF ? NU : 1];
-  const uint8_t* src = nullptr;   // the row's codes, null when there is no such row
+  auto page_at = [&](int row) -> int { return row >= 0 ? bt[row / P] : -1; };
+  uint32_t nraw[W];
+  float nsc[NU], nbi[AFF ? NU : 1];
+  const uint8_t* src = nullptr;   // codes of the row being loaded; null: no such row
+  bool nskip = false;
   auto load_piece = [&](int p) {
+    const uint4* s = reinterpret_cast<const uint4*>(src + p * (4 * W));
 #pragma unroll
-    for (int i = 0; i < PB * BW / 4; ++i) {
-      const uint4 x = src ? __ldg(reinterpret_cast<const uint4*>(src + p * (PB * BW * 4)) + i) : make_uint4(0, 0, 0, 0);
-      raw[4 * i] = x.x;
-      raw[4 * i + 1] = x.y;
-      raw[4 * i + 2] = x.z;
-      raw[4 * i + 3] = x.w;
+    for (int x = 0; x < W / 4; ++x) {
+      const uint4 y = src ? __ldg(s + x) : make_uint4(0, 0, 0, 0);
+      nraw[4 * x] = y.x;
+      nraw[4 * x + 1] = y.y;
+      nraw[4 * x + 2] = y.z;
+      nraw[4 * x + 3] = y.w;
     }
   };
-  bool skip = false;
-  auto load_row = [&](int row, int page) {
-    skip = false;
-    src = nullptr;
-    const uint8_t* par = nullptr;
-    if (row >= 0) {
-      if (page < 0 || page >= a.n_pool_pages) {
-        skip = true;
-        report(a.status, KVQ_DEV_BAD_PAGE);
-      } else {
-        const uint8_t* sub = pool + page * L.page_bytes;
-        src = sub + (row % P) * L.code_bytes;
-        par = sub + P * L.code_bytes + (row % P) * L.param_row_bytes;
-      }
-    }
-    load_piece(0);
+  auto open_row = [&](int row, int page) {   // parameters, and where the codes are
+    nskip = row >= 0 && (page < 0 || page >= a.n_pool_pages);
+    if (nskip) report(a.status, KVQ_DEV_BAD_PAGE);
+    const bool there = row >= 0 && !nskip;
+    const uint8_t* sub = pool + (there ? page : 0) * L.page_bytes;
+    src = there ? sub + (row % P) * L.code_bytes : nullptr;
     if constexpr (!F16) {
+      const uint8_t* par = sub + P * L.code_bytes + (there ? row % P : 0) * L.param_row_bytes;
 #pragma unroll
       for (int u = 0; u < NU; ++u) {
-        if (u % gu == 0) {
+        nsc[u] = u ? nsc[u - (u > 0)] : 0.f;
+        if constexpr (AFF) nbi[u] = u ? nbi[u - (u > 0)] : 0.f;
+        if (there && u % gu == 0) {
           const int g = u / gu;
-          sc[u] = par ? load_param(par + (AFF ? 2 * g : g) * pb, L.param) : 0.f;
-          if constexpr (AFF) bi[u] = par ? load_param(par + (2 * g + 1) * pb, L.param) : 0.f;
-        } else {
-          sc[u] = sc[u - (u > 0)];
-          if constexpr (AFF) bi[u] = bi[u - (u > 0)];
+          nsc[u] = load_param(par + (AFF ? 2 * g : g) * pb, L.param);
+          if constexpr (AFF) nbi[u] = load_param(par + (2 * g + 1) * pb, L.param);
         }
       }
     }
   };
 
-  int held = IS_V ? -100 : 0;   // V: the exponent held so far
+  int held = IS_V && !F16 ? -100 : 0;   // V: the exponent held so far
   int row = row_at(0);
-  load_row(row, row >= 0 ? bt[row / P] : -1);
+  open_row(row, page_at(row));
+  load_piece(0);
+  int row1 = row_at(1);
+  int page1 = page_at(row1);
+#pragma unroll 1
   for (int i = 0; i < n; ++i) {
-    const int row_next = row_at(i + 1);
-    const int page_next = row_next >= 0 ? bt[row_next / P] : -1;
+    const int row2 = row_at(i + 2);
+    const int page2 = page_at(row2);
     StepMeta& meta = (IS_V ? sh.vm : sh.km)[i % kSlots];
+    const bool skip = nskip;
     bool bad = false;
-    float down = 1.f;
+    __half2 sc[NU], bi[AFF ? NU : 1];
     if constexpr (!F16) {
       // the largest magnitude of the step's values
       float amp = 0.f;
 #pragma unroll
       for (int u = 0; u < NU; ++u) {
         float x;
-        if constexpr (AFF) x = fmaxf(fabsf(bi[u]), fabsf(fmaf(15.f, sc[u], bi[u])));
-        else x = fabsf(sc[u]) * (KIND == KVQ_SYM_INT8 ? 127.f : 8.f);
-        bad |= !(x <= 3.0e38f) || !isfinite(sc[u]);
+        if constexpr (AFF) x = fmaxf(fabsf(nbi[u]), fabsf(fmaf(15.f, nsc[u], nbi[u])));
+        else x = fabsf(nsc[u]) * (KIND == KVQ_SYM_INT8 ? 127.f : 8.f);
+        bad |= !(x <= 3.0e38f) || !isfinite(nsc[u]);
         amp = fmaxf(amp, x);
       }
-      if (bad) amp = 0.f;
-      const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(amp));
+      const bool gone = bad || src == nullptr;
+      const uint32_t top = __reduce_max_sync(0xffffffffu, gone ? 0u : __float_as_uint(amp));
       if (lane == 0) sh.red[IS_V][i & 1][warp] = top;
       group_sync(IS_V ? 2 : 1);
       const uint32_t* r = sh.red[IS_V][i & 1];
       const int e = hold_exponent(__uint_as_float(max(max(r[0], r[1]), max(r[2], r[3]))));
       held = IS_V ? max(held, e) : e;
-      down = pow2i(-held);
-    } else {
-      held = 0;
+      const float down = pow2i(-held);
+#pragma unroll
+      for (int u = 0; u < NU; ++u) {
+        sc[u] = __float2half2_rn(gone ? 0.f : nsc[u] * down);
+        if constexpr (AFF) bi[u] = __float2half2_rn(gone ? 0.f : nbi[u] * down);
+      }
     }
-    const bool gone = bad || src == nullptr;
-    if (!F16 || !IS_V) {
+    auto publish = [&]() {
       const uint32_t ws = __ballot_sync(0xffffffffu, skip), wb = __ballot_sync(0xffffffffu, bad);
       if (lane == 0) {
         meta.skip[warp] = ws;
         meta.bad[warp] = wb;
         if (warp == 0) meta.e = held;
-        if (IS_V) mbar_arrive(smem_u32(&sh.vmeta[i % kSlots]));
+        mbar_arrive(smem_u32(&ready[i % kSlots]));
       }
-    }
+    };
+    if constexpr (!F16) publish();
 #pragma unroll
-    for (int h = 0; h < HB; ++h) {
-      const int c = i * HB + h, st = c % kStages;
-      mbar_wait(smem_u32(&empty[st]), (c / kStages + 1) & 1, stop);
-      const uint32_t dst = ring + st * kBlockBytes + pt * 128;
-      const uint32_t* w = raw + (h % PB) * BW;
-      if constexpr (F16) {
-        uint32_t inf = 0;   // a half with all exponent bits set carries into its sign bit
+    for (int p = 0; p < NP; ++p) {
+      uint32_t raw[W];
 #pragma unroll
-        for (int x = 0; x < BW; ++x) inf |= ((w[x] & 0x7FFF7FFFu) + 0x04000400u) & 0x80008000u;
-        bad |= inf != 0;
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          const uint32_t at = dst + ((x ^ (pt & 7)) << 4);
-          const bool z = inf != 0;
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(z ? 0u : w[4 * x]),
-                       "r"(z ? 0u : w[4 * x + 1]), "r"(z ? 0u : w[4 * x + 2]), "r"(z ? 0u : w[4 * x + 3])
-                       : "memory");
-        }
-        if (h == HB - 1) {   // known only now
-          const uint32_t wb = __ballot_sync(0xffffffffu, bad);
-          if (lane == 0) {
-            meta.bad[warp] = wb;
-            if (IS_V) {
-              meta.skip[warp] = 0;
-              if (warp == 0) meta.e = 0;
-              mbar_arrive(smem_u32(&sh.vmeta[i % kSlots]));
-            }
-          }
-        }
+      for (int x = 0; x < W; ++x) raw[x] = nraw[x];
+      if (p == NP - 1) {
+        open_row(row1, page1);
+        load_piece(0);
       } else {
+        load_piece(p + 1);
+      }
+#pragma unroll
+      for (int b = 0; b < PB; ++b) {
+        const int h = p * PB + b;
+        const int c = i * HB + h, st = c % kStages;
+        mbar_wait(smem_u32(&empty[st]), (c / kStages + 1) & 1, stop);
+        const uint32_t dst = ring + st * kBlockBytes;
+        const uint32_t* w = raw + b * BW;
+        bool zero = false;
+        if constexpr (F16) {
+          uint32_t inf = 0;   // a half with all exponent bits set carries into its sign bit
+#pragma unroll
+          for (int x = 0; x < BW; ++x) inf |= ((w[x] & 0x7FFF7FFFu) + 0x04000400u) & 0x80008000u;
+          zero = inf != 0;
+          bad |= zero;
+        }
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
-          const int u = (64 * h + 8 * x) / 32;
-          const float s = gone ? 0.f : sc[u] * down, b = AFF && !gone ? bi[AFF ? u : 0] * down : 0.f;
+          const int u = F16 ? 0 : (64 * h + 8 * x) / 32;
           uint4 y;
-          if constexpr (KIND == KVQ_SYM_INT8)
-            y = dequant8<KIND>(w[2 * x], w[2 * x + 1], __float2half2_rn(s), __float2half2_rn(b));
+          if constexpr (F16)
+            y = zero ? make_uint4(0, 0, 0, 0) : make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+          else if constexpr (KIND == KVQ_SYM_INT8)
+            y = dequant8<KIND>(w[2 * x], w[2 * x + 1], sc[u], sc[u]);
           else
-            y = dequant8<KIND>(w[x], 0, __float2half2_rn(s), __float2half2_rn(b));
+            y = dequant8<KIND>(w[x], 0, sc[u], bi[AFF ? u : 0]);
           const uint32_t at = dst + ((x ^ (pt & 7)) << 4);
           asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w)
                        : "memory");
         }
+        if (F16 && h == HB - 1) publish();   // known only now
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&full[st]));
       }
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&full[st]));
-      // the next loads are in flight while this warpgroup waits for a free block
-      if (h == HB - 1) load_row(row_next, page_next);
-      else if ((h + 1) % PB == 0) load_piece((h + 1) / PB);
     }
+    row1 = row2;
+    page1 = page2;
   }
 }
 
@@ -497,7 +498,10 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
       mbar_init(smem_u32(&sh.kempty[i]), 1);
       mbar_init(smem_u32(&sh.vempty[i]), 1);
     }
-    for (int i = 0; i < kSlots; ++i) mbar_init(smem_u32(&sh.vmeta[i]), 4);
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(smem_u32(&sh.kmeta[i]), 4);
+      mbar_init(smem_u32(&sh.vmeta[i]), 4);
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&sh.qfull[i]), 4);
       mbar_init(smem_u32(&sh.sfull[i]), 1);
@@ -534,10 +538,11 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
         const int buf = MT == 2 ? rt : i & 1;
         const uint32_t s_at = tmem + lanes + s_col + buf * 128;
         const StepMeta &km = sh.km[i % kSlots], &vm = sh.vm[i % kSlots];
-        mbar_wait(smem_u32(&sh.sfull[buf]), MT == 2 ? i & 1 : (i >> 1) & 1, stop);
+        // everything but the scores first
+        mbar_wait(smem_u32(&sh.kmeta[i % kSlots]), (i / kSlots) & 1, stop);
         mbar_wait(smem_u32(&sh.vmeta[i % kSlots]), (i / kSlots) & 1, stop);
-        tc_fence_after();
         const float f = fmaxf(qs * pow2i(km.e), 1.17549435e-38f);   // never 0: -inf stays -inf
+        const int ve = vm.e;
         const int tb = kr.base<kKeys>(j0 + i), end = kr.end(j0 + i);
         uint32_t odd = 0;
 #pragma unroll
@@ -551,35 +556,11 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
         mask.skip = km.skip;
         mask.kbad = km.bad;
         mask.vbad = vm.bad;
+        mbar_wait(smem_u32(&sh.sfull[buf]), MT == 2 ? i & 1 : (i >> 1) & 1, stop);
+        tc_fence_after();
 
-        // the row's maximum; columns 64 .. 127 stay in registers
-        float x0[32], x1[32];
-        float mx = -INFINITY;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          tmem_ld32(s_at + 64 * half, x0);
-          tmem_ld32(s_at + 64 * half + 32, x1);
-          tmem_ld_wait(x0);
-          tmem_ld_wait(x1);
-          if (!whole) {
-            mask.apply(2 * half, x0);
-            mask.apply(2 * half + 1, x1);
-          }
-#pragma unroll
-          for (int c = 0; c < 32; ++c) mx = fmaxf(mx, fmaxf(x0[c], x1[c]));
-        }
-        mx *= f;
-        const bool raise = mx > m + kLazy;
-        const float mn = raise ? mx : m;
-        if (i == 0) {
-          m = mn;
-          held = vm.e;
-        } else if (__any_sync(0xffffffffu, raise || vm.e != held)) {
-          const float c = raise ? ex2(m - mn) : 1.f;   // 2^-inf = 0: no key so far
-          l *= c;
-          const float co = c * pow2i(held - vm.e);
-          m = mn;
-          held = vm.e;
+        // O of the steps before, times a power of two a row.
+        auto scale_o = [&](float c) {
           // O is at rest: with two row tiles this step's scores were issued
           // after the last step's O; with one, they were issued before it, but
           // after that of the step before, so the parity is not ambiguous
@@ -593,34 +574,66 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
             tmem_ld32(o_at + d, o);
             tmem_ld_wait(o);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] *= co;
+            for (int e = 0; e < 32; ++e) o[e] *= c;
             tmem_st32(o_at + d, o);
           }
+        };
+        if (ve != held) {   // the same for every row
+          if (i > 0) scale_o(pow2i(held - ve));
+          held = ve;
         }
-        const float sub = m == -INFINITY ? 0.f : m - kShift;
-        // P over columns 64 .. 127 of S, 16 words for 32 keys
-        auto weights = [&](int c, const float (&x)[32]) {
+        // One pass over the scores, 32 at a time: P takes the place of S, half
+        // its width, behind the reads.  The running maximum rises, by whole
+        // powers of two, where a row's scores pass it by more than 2^8; what
+        // P the step already has is scaled with O.
+        uint64_t sum = pack2(l, 0.f);
+        const uint64_t f2 = pack2(f, f);
+        float sub = m == -INFINITY ? 0.f : m - kShift;
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          float x[32];
+          tmem_ld32(s_at + 32 * c, x);
+          tmem_ld_wait(x);
+          if (!whole) mask.apply(c, x);
+          float mx = fmaxf(x[0], x[1]);
+#pragma unroll
+          for (int k = 2; k < 32; k += 2) mx = fmaxf(mx, fmaxf(x[k], x[k + 1]));
+          mx *= f;
+          const bool raise = mx > m + kLazy;
+          if (__any_sync(0xffffffffu, raise)) {
+            const float mn = raise ? (m == -INFINITY ? mx : m + ceilf(mx - m)) : m;
+            const float co = raise ? (m == -INFINITY ? 0.f : pow2i((int)(m - mn))) : 1.f;
+            m = mn;
+            sub = m == -INFINITY ? 0.f : m - kShift;
+            const float2 s2 = unpack2(sum);
+            sum = pack2(s2.x * co, s2.y * co);
+            const __half2 c2 = __float2half2_rn(co);
+            tmem_st_wait();   // P written so far is read back
+#pragma unroll 1
+            for (int d = 0; d < c; ++d) {
+              uint32_t w[16];
+              tmem_ld16_wait(s_at + 16 * d, w);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) w[k] = h2u(__hmul2(u2h(w[k]), c2));
+              tmem_st16(s_at + 16 * d, w);
+            }
+            if (i > 0) scale_o(co);
+          }
+          const uint64_t sub2 = pack2(-sub, -sub);
           uint32_t w[16];
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
-            const float p0 = ex2(fmaf(x[2 * k], f, -sub)), p1 = ex2(fmaf(x[2 * k + 1], f, -sub));
-            l += p0 + p1;
+            const float2 y = unpack2(fma2(pack2(x[2 * k], x[2 * k + 1]), f2, sub2));
+            const float p0 = ex2(y.x), p1 = ex2(y.y);
+            sum = add2(sum, pack2(p0, p1));
             w[k] = h2u(__floats2half2_rn(p0, p1));
           }
-          tmem_st16(s_at + 64 + 16 * c, w);
-        };
-        weights(2, x0);
-        tmem_ld32(s_at, x0);
-        weights(3, x1);
-        tmem_ld32(s_at + 32, x1);
-        tmem_ld_wait(x0);
-        tmem_ld_wait(x1);
-        if (!whole) {
-          mask.apply(0, x0);
-          mask.apply(1, x1);
+          tmem_st16(s_at + 16 * c, w);
         }
-        weights(0, x0);
-        weights(1, x1);
+        {
+          const float2 s2 = unpack2(sum);
+          l = s2.x + s2.y;
+        }
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
@@ -693,7 +706,9 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
     // ------------------------------------------------------------ products
     if (lane == 0) {
     constexpr uint32_t id_qk = idesc_f16(kKeys, false), id_pv = idesc_f16(PVN, true);
-    const uint32_t qb = smem_u32(sh.q), kb = smem_u32(sh.k), vb = smem_u32(sh.v);
+    // descriptors count addresses in 16 bytes
+    const uint64_t qd = smem_desc(smem_u32(sh.q), 16), kd = smem_desc(smem_u32(sh.k), 16),
+                   vd = smem_desc(smem_u32(sh.v), kBlockBytes);
     auto wait_full = [&](uint64_t* full, int c) {
       mbar_wait(smem_u32(&full[c % kStages]), (c / kStages) & 1, stop);
     };
@@ -709,8 +724,8 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
         tc_fence_after();
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          mma_ss(tmem + s_col + buf * 128, smem_desc(qb + (rt * HB + h) * kBlockBytes + 32 * k, 16),
-                 smem_desc(kb + (c % kStages) * kBlockBytes + 32 * k, 16), id_qk, h > 0 || k > 0);
+          mma_ss(tmem + s_col + buf * 128, qd + ((rt * HB + h) * kBlockBytes + 32 * k) / 16,
+                 kd + ((c % kStages) * kBlockBytes + 32 * k) / 16, id_qk, h > 0 || k > 0);
         if (rt == lt) mma_commit(smem_u32(&sh.kempty[c % kStages]));
       }
       mma_commit(smem_u32(&sh.sfull[buf]));
@@ -727,8 +742,8 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
         tc_fence_after();
 #pragma unroll
         for (int k = 0; k < kKeys / 16; ++k)
-          mma_ts(tmem + o_col + rt * HD + 64 * h, tmem + s_col + buf * 128 + 64 + 8 * k,
-                 smem_desc(vb + (c % kStages) * kBlockBytes + 2048 * k, kBlockBytes), id_pv, i > 0 || k > 0);
+          mma_ts(tmem + o_col + rt * HD + 64 * h, tmem + s_col + buf * 128 + 8 * k,
+                 vd + ((c % kStages) * kBlockBytes + 2048 * k) / 16, id_pv, i > 0 || k > 0);
         if (rt == lt) {
 #pragma unroll
           for (int b = 0; b < PVN / 64; ++b) mma_commit(smem_u32(&sh.vempty[(c + b) % kStages]));

@@ -23,12 +23,15 @@ __device__ __forceinline__ void mbar_init_fence() {
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// Tests the phase of that parity; the thread sleeps in hardware until it is
+// done, or about a millisecond.
+constexpr uint32_t kTryNs = 1000000;
 __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
-      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.b32 %0, 1, 0, p;\n}\n"
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.b32 %0, 1, 0, p;\n}\n"
       : "=r"(ok)
-      : "r"(bar), "r"(parity)
+      : "r"(bar), "r"(parity), "r"(kTryNs)
       : "memory");
   return ok != 0;
 }
@@ -40,22 +43,42 @@ __device__ __forceinline__ uint64_t now_ns() {
 // Waits for the phase of that parity, two seconds at most; *stop is raised
 // when the time runs out and ends every other wait of the CTA too.
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
-__device__ __noinline__ bool mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int* stop) {
+static __device__ __noinline__ void mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int* stop) {
   const uint64_t t0 = now_ns();
   while (!mbar_try(bar, parity)) {
-    if (*stop) return false;
+    if (*stop) return;
     if (now_ns() - t0 > kWaitLimitNs) {
       *stop = 1;
-      return false;
+      return;
     }
   }
-  return true;
 }
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* stop) {
-#pragma unroll 1
-  for (int i = 0; i < 16; ++i)
-    if (mbar_try(bar, parity)) return true;
-  return mbar_wait_slow(bar, parity, stop);
+__device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, volatile int* stop) {
+  if (!mbar_try(bar, parity)) mbar_wait_slow(bar, parity, stop);
+}
+
+// ---------------------------------------------------------------- pairs of fp32
+// Two fp32 operations an instruction, each rounded as the single one.
+
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 // ---------------------------------------------------------------- fences
@@ -112,6 +135,16 @@ __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&x)[16]
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
       "%14, %15};" ::KVQ_I8(x, 0),
       KVQ_I8(x, 8), "r"(addr)
+      : "memory");
+}
+// 16 columns, as words.
+__device__ __forceinline__ void tmem_ld16_wait(uint32_t addr, uint32_t (&x)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15}, [%16];\n tcgen05.wait::ld.sync.aligned;"
+      : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7]), "=r"(x[8]),
+        "=r"(x[9]), "=r"(x[10]), "=r"(x[11]), "=r"(x[12]), "=r"(x[13]), "=r"(x[14]), "=r"(x[15])
+      : "r"(addr)
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
