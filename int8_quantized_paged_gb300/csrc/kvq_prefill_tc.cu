@@ -456,7 +456,7 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
 
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   // block index: kv head fastest, then the split, then the tile, last tiles (the longest key ranges) first
   const int kvh = blockIdx.x % a.n_kv_heads, rest = blockIdx.x / a.n_kv_heads;
   const int split = rest % a.n_splits, x = a.n_tiles - 1 - rest / a.n_splits;
@@ -704,7 +704,10 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
     produce_kind<HD, true>(a.vl.kind, a, t, kr, j0, n, kvh, tid - 128 * MT - 128, sh, stop);
   } else {
     // ------------------------------------------------------------ products
-    if (lane == 0) {
+    // The whole warp walks the steps and one lane issues: the descriptors then
+    // stay in uniform registers, where the instruction takes them (a lone lane
+    // in a branch of its own spent 120 cycles on each product, twice its length).
+    const bool leader = elect_one();
     constexpr uint32_t id_qk = idesc_f16(kKeys, false), id_pv = idesc_f16(PVN, true);
     // descriptors count addresses in 16 bytes
     const uint64_t qd = smem_desc(smem_u32(sh.q), 16), kd = smem_desc(smem_u32(sh.k), 16),
@@ -722,13 +725,16 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
         const int c = i * HB + h;
         wait_full(sh.kfull, c);
         tc_fence_after();
+        if (leader) {
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           mma_ss(tmem + s_col + buf * 128, qd + ((rt * HB + h) * kBlockBytes + 32 * k) / 16,
                  kd + ((c % kStages) * kBlockBytes + 32 * k) / 16, id_qk, h > 0 || k > 0);
         if (rt == lt) mma_commit(smem_u32(&sh.kempty[c % kStages]));
+        if (h == HB - 1) mma_commit(smem_u32(&sh.sfull[buf]));
+        }
+        __syncwarp();
       }
-      mma_commit(smem_u32(&sh.sfull[buf]));
     };
     // O of row tile rt, step i
     auto pv = [&](int rt, int i, int nt) {
@@ -740,6 +746,7 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
 #pragma unroll
         for (int b = 0; b < PVN / 64; ++b) wait_full(sh.vfull, c + b);
         tc_fence_after();
+        if (leader) {
 #pragma unroll
         for (int k = 0; k < kKeys / 16; ++k)
           mma_ts(tmem + o_col + rt * HD + 64 * h, tmem + s_col + buf * 128 + 8 * k,
@@ -748,8 +755,10 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
 #pragma unroll
           for (int b = 0; b < PVN / 64; ++b) mma_commit(smem_u32(&sh.vempty[(c + b) % kStages]));
         }
+        if (h + PVN / 64 >= HB && (MT == 1 || i == nt - 1)) mma_commit(smem_u32(&sh.ofull[rt]));
+        }
+        __syncwarp();
       }
-      if (MT == 1 || i == nt - 1) mma_commit(smem_u32(&sh.ofull[rt]));
     };
     for (int rt = 0; rt < na; ++rt) {
       mbar_wait(smem_u32(&sh.qfull[rt]), 0, stop);
@@ -768,11 +777,10 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
         }
       }
     }
-    mma_commit(smem_u32(&sh.drain));
+    if (leader) mma_commit(smem_u32(&sh.drain));
+    __syncwarp();
     mbar_wait(smem_u32(&sh.drain), 0, stop);
     tc_fence_before();
-    }
-    __syncwarp();
   }
   __syncthreads();
   if (tid == 0 && sh.stop) report(a.status, KVQ_DEV_TIMEOUT);
