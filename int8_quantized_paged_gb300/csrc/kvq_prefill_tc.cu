@@ -9,7 +9,7 @@
 //   O += P V'     (P from tensor memory, V' from shared memory)
 // Roles, by warp: MT warpgroups of softmax (a thread owns a row: no shuffles),
 // one warpgroup that dequantizes K and one that dequantizes V (a thread owns a
-// key), and a warp whose first lane issues the products.  They meet at
+// key), and a warp that issues the products.  They meet at
 // mbarriers only.  With two row tiles the products of one run while the other's
 // softmax does; head_dim 256 has room for one row tile in tensor memory, so its
 // S is double-buffered instead.
@@ -59,7 +59,23 @@ constexpr float kLazy = 8.0f;            // the running maximum rises past +2^8 
 constexpr float kShift = 7.0f;           // P is held times 2^7
 
 __host__ __device__ constexpr int row_tiles(int hd) { return hd == 256 ? 1 : 2; }
-__host__ __device__ constexpr int tc_threads(int hd) { return 128 * row_tiles(hd) + 256 + 32; }
+// Blocks that change hands together: a whole step's, or at head_dim 256, where
+// the ring holds one step only, one.
+__host__ __device__ constexpr int unit_blocks(int hd) { return hd == 256 ? 1 : hd / 64; }
+__host__ __device__ constexpr int tc_threads(int hd) { return 128 * row_tiles(hd) + 256 + 128; }
+// Registers a thread: at launch (65536 over the threads, in eights), then by
+// role.  A role may only take what the others gave back, so the shares must
+// not exceed the launch's: (softmax * tiles + 2 producers + products) * 128.
+__host__ __device__ constexpr int regs_launch(int hd) { return 65536 / tc_threads(hd) / 8 * 8; }
+__host__ __device__ constexpr int regs_softmax(int hd) { return hd == 256 ? 208 : 152; }
+__host__ __device__ constexpr int regs_produce(int hd) { return hd == 256 ? 120 : 72; }
+constexpr int kRegsProducts = 32;
+template <int HD>
+constexpr bool split_fits() {
+  return regs_softmax(HD) * row_tiles(HD) + 2 * regs_produce(HD) + kRegsProducts <=
+         regs_launch(HD) * (tc_threads(HD) / 128);
+}
+static_assert(split_fits<64>() && split_fits<128>() && split_fits<256>(), "register split");
 
 // What the softmax needs to know about a step's keys.
 struct StepMeta {
@@ -78,12 +94,12 @@ struct Shared {
   uint8_t v[kStages * kBlockBytes];
   StepMeta km[kSlots], vm[kSlots];
   float qscale[MT * 128];   // f without the keys' part
-  uint32_t red[2][2][4];
-  uint64_t kfull[kStages], kempty[kStages], vfull[kStages], vempty[kStages];
+  int red[2][2][4];
+  uint64_t kfull[kStages], kempty[kStages], vfull[kStages], vempty[kStages];   // a unit each
   uint64_t kmeta[kSlots], vmeta[kSlots];   // a step's metadata are there
   uint64_t qfull[2], sfull[2], pfull[2];
   uint64_t ofull[2];   // O of a row tile: its last step (two row tiles), or every step (one)
-  uint64_t drain;
+  uint64_t drain[2];
   uint32_t tmem;
   int stop;
 };
@@ -93,12 +109,16 @@ constexpr size_t shared_bytes() { return sizeof(Shared<HD>) + 1024; }   // the b
 __device__ __forceinline__ float pow2i(int e) {   // 2^e, 0 below 2^-126
   return e < -126 ? 0.f : __int_as_float((e + 127) << 23);
 }
-// The exponent that holds magnitudes up to x (finite, >= 0) in [2^14, 2^15),
-// as far as both factors stay normal floats.
-__device__ __forceinline__ int hold_exponent(float x) {
-  const int e = (int)(__float_as_uint(x) >> 23) - 127 - 14;
-  return min(max(e, -100), 112);
+// Exponents at which operands are held, as far as both factors stay normal
+// floats: magnitudes up to x (finite, >= 0) in [2^14, 2^15) ...
+__device__ __forceinline__ int exponent_of(float x) { return (int)(__float_as_uint(x) >> 23) - 127; }
+__device__ __forceinline__ int hold_exponent(float x) { return min(max(exponent_of(x) - 14, -100), 112); }
+// ... and a key's scales up to s in [2^-9, 2^-8) and biases up to b below 2^15
+// (dequant8 multiplies subnormals by 2^24 s).
+__device__ __forceinline__ int key_exponent(float s, float b) {
+  return max(max(exponent_of(s) + 9, exponent_of(b) - 14), -100);
 }
+constexpr float kMostScale = 1.0e35f;   // held at 2^126 at most: a larger scale counts as not finite
 __device__ __forceinline__ void group_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
 
 __device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
@@ -117,51 +137,59 @@ __host__ __device__ constexpr int pos_of(int order, int d) {
   return order == 0 ? d : (order == 1 ? (d & 4) | ((d & 1) << 1) | ((d >> 1) & 1) : ((d & 3) << 1) | (d >> 2));
 }
 
-// Eight codes (one word; two words for 8-bit kinds) to eight fp16 values
-// s * code (+ b), in order_of(KIND).
+// A group's scale and bias for dequant8.
+struct Scale {
+  __half2 lo, hi, b;
+};
 template <int KIND>
-__device__ __forceinline__ uint4 dequant8(uint32_t w0, uint32_t w1, __half2 s, __half2 b) {
+__device__ __forceinline__ Scale make_scale(float s, float b) {   // s < 2^-8
+  const __half2 h = __float2half2_rn(s);                           // the stored scale, to fp16
+  Scale r;
+  r.lo = __hmul2(h, __float2half2_rn(4096.f));                     // 2^24 s, exact
+  r.lo = __hmul2(r.lo, __float2half2_rn(4096.f));
+  r.hi = __hmul2(r.lo, __float2half2_rn(0.0625f));
+  if (KIND == KVQ_AFFINE_INT4) r.b = __float2half2_rn(b);
+  else r.b = __hmul2(h, __float2half2_rn(KIND == KVQ_SYM_INT8 ? -128.f : -8.f));
+  return r;
+}
+// Eight codes (one word; two words for 8-bit kinds) to eight fp16 values
+// s * code + b, in order_of(KIND).  An unsigned code n in the low bits of a
+// half is the subnormal n 2^-24, and one multiply-add by 2^24 s makes it n s +
+// b, rounded once; signed codes are n - 8 (n - 128).  The high nibble of a byte
+// is 16 n.
+template <int KIND>
+__device__ __forceinline__ uint4 dequant8(uint32_t w0, uint32_t w1, const Scale& s) {
   uint32_t r[4];
   if constexpr (KIND == KVQ_SYM_INT8) {
-    const __half2 off = u2h(0x64806480u);   // 1024 + 128
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const uint32_t w = i ? w1 : w0;
-      r[2 * i] = h2u(__hmul2(__hsub2(u2h((w & 0x00FF00FFu) ^ 0x64806480u), off), s));
-      r[2 * i + 1] = h2u(__hmul2(__hsub2(u2h(((w >> 8) & 0x00FF00FFu) ^ 0x64806480u), off), s));
+      r[2 * i] = h2u(__hfma2(u2h((w & 0x00FF00FFu) ^ 0x00800080u), s.lo, s.b));
+      r[2 * i + 1] = h2u(__hfma2(u2h(((w >> 8) & 0x00FF00FFu) ^ 0x00800080u), s.lo, s.b));
     }
   } else {
-    constexpr bool SYM = KIND == KVQ_SYM_INT4, AFF = KIND == KVQ_AFFINE_INT4;
-    // low nibble of a byte: 1024 + n; high nibble: 1024 + 16 n, brought back by
-    // an exact fused multiply-add; n = code + 8 but for affine codes
-    constexpr uint32_t ml = SYM ? 0x64086408u : 0x64006400u, mh = SYM ? 0x64806480u : 0x64006400u;
-    const __half2 lo = u2h(AFF ? 0x64006400u : 0x64086408u);               // 1024 (+ 8)
-    const __half2 hi = AFF ? __floats2half2_rn(-64.f, -64.f) : __floats2half2_rn(-72.f, -72.f);
-    const __half2 six = __floats2half2_rn(0.0625f, 0.0625f);
-    const uint32_t w1s = w0 >> 8;
-    __half2 c[4];
-    c[0] = __hsub2(u2h((w0 & 0x000F000Fu) ^ ml), lo);
-    c[1] = __hfma2(u2h((w0 & 0x00F000F0u) ^ mh), six, hi);
-    c[2] = __hsub2(u2h((w1s & 0x000F000Fu) ^ ml), lo);
-    c[3] = __hfma2(u2h((w1s & 0x00F000F0u) ^ mh), six, hi);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = h2u(AFF ? __hfma2(c[i], s, b) : __hmul2(c[i], s));
+    constexpr uint32_t fl = KIND == KVQ_SYM_INT4 ? 0x00080008u : 0u, fh = KIND == KVQ_SYM_INT4 ? 0x00800080u : 0u;
+    const uint32_t ws = w0 >> 8;
+    r[0] = h2u(__hfma2(u2h((w0 & 0x000F000Fu) ^ fl), s.lo, s.b));
+    r[1] = h2u(__hfma2(u2h((w0 & 0x00F000F0u) ^ fh), s.hi, s.b));
+    r[2] = h2u(__hfma2(u2h((ws & 0x000F000Fu) ^ fl), s.lo, s.b));
+    r[3] = h2u(__hfma2(u2h((ws & 0x00F000F0u) ^ fh), s.hi, s.b));
   }
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
 // The dequantizing warpgroup of K or V: thread pt owns key pt of every step.
 // Loads run ahead of their use: a step's page id two steps, its parameters one
-// step, and its codes one piece (16 words of a row, two blocks of 4-bit codes).
+// step, and its codes one piece (16 words of a row).
 template <int KIND, int HD, bool IS_V>
 __device__ void produce(const PrefillArgs& a, const PrefillTile& t, const KeyRange& kr, int j0, int n, int kvh, int pt,
                         Shared<HD>& sh, volatile int* stop) {
-  constexpr int P = 16, HB = HD / 64;
+  constexpr int P = 16, HB = HD / 64, UB = unit_blocks(HD);
   constexpr bool F16 = KIND == KVQ_F16_KV, AFF = KIND == KVQ_AFFINE_INT4;
-  constexpr int BW = F16 ? 32 : (KIND == KVQ_SYM_INT8 ? 16 : 8);   // words of a block's codes
-  constexpr int PB = BW == 8 && HB > 1 ? 2 : 1;                    // blocks a piece
-  constexpr int NP = HB / PB;                                      // pieces a row
-  constexpr int W = PB * BW;
+  constexpr int CW = F16 ? 4 : (KIND == KVQ_SYM_INT8 ? 2 : 1);     // words of eight codes
+  constexpr int W = CW * HD / 8 < 16 ? CW * HD / 8 : 16;           // words of a piece
+  constexpr int NP = CW * HD / 8 / W;                              // pieces a row
+  constexpr int CP = W / CW;                                       // eights a piece
   constexpr int NU = F16 ? 1 : HD / 32;                            // 32-dim units: groups are 32 dims or more
   const PoolLayout& L = IS_V ? a.vl : a.kl;
   const uint8_t* pool = (IS_V ? a.v_pool : a.k_pool) + (int64_t)kvh * L.sub_bytes;
@@ -230,30 +258,30 @@ __device__ void produce(const PrefillArgs& a, const PrefillTile& t, const KeyRan
     StepMeta& meta = (IS_V ? sh.vm : sh.km)[i % kSlots];
     const bool skip = nskip;
     bool bad = false;
-    __half2 sc[NU], bi[AFF ? NU : 1];
+    float sc[NU], bi[AFF ? NU : 1];
+    bool gone = src == nullptr;
     if constexpr (!F16) {
-      // the largest magnitude of the step's values
-      float amp = 0.f;
+      // the largest scale and bias of the step's keys
+      float ms = 0.f, mb = 0.f;
 #pragma unroll
       for (int u = 0; u < NU; ++u) {
-        float x;
-        if constexpr (AFF) x = fmaxf(fabsf(nbi[u]), fabsf(fmaf(15.f, nsc[u], nbi[u])));
-        else x = fabsf(nsc[u]) * (KIND == KVQ_SYM_INT8 ? 127.f : 8.f);
-        bad |= !(x <= 3.0e38f) || !isfinite(nsc[u]);
-        amp = fmaxf(amp, x);
+        bad |= !(nsc[u] < kMostScale) || (AFF && !isfinite(nbi[AFF ? u : 0]));
+        ms = fmaxf(ms, nsc[u]);
+        if constexpr (AFF) mb = fmaxf(mb, fabsf(nbi[u]));
       }
-      const bool gone = bad || src == nullptr;
-      const uint32_t top = __reduce_max_sync(0xffffffffu, gone ? 0u : __float_as_uint(amp));
+      gone |= bad;
+      const int e1 = gone ? -100 : key_exponent(ms, mb);
+      const int top = __reduce_max_sync(0xffffffffu, e1);
       if (lane == 0) sh.red[IS_V][i & 1][warp] = top;
       group_sync(IS_V ? 2 : 1);
-      const uint32_t* r = sh.red[IS_V][i & 1];
-      const int e = hold_exponent(__uint_as_float(max(max(r[0], r[1]), max(r[2], r[3]))));
+      const int* r = sh.red[IS_V][i & 1];
+      const int e = max(max(r[0], r[1]), max(r[2], r[3]));
       held = IS_V ? max(held, e) : e;
       const float down = pow2i(-held);
 #pragma unroll
       for (int u = 0; u < NU; ++u) {
-        sc[u] = __float2half2_rn(gone ? 0.f : nsc[u] * down);
-        if constexpr (AFF) bi[u] = __float2half2_rn(gone ? 0.f : nbi[u] * down);
+        sc[u] = gone ? 0.f : nsc[u] * down;
+        if constexpr (AFF) bi[u] = gone ? 0.f : nbi[u] * down;
       }
     }
     auto publish = [&]() {
@@ -266,6 +294,8 @@ __device__ void produce(const PrefillArgs& a, const PrefillTile& t, const KeyRan
       }
     };
     if constexpr (!F16) publish();
+    bool zero = false;
+    Scale s = {};
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
       uint32_t raw[W];
@@ -278,38 +308,37 @@ __device__ void produce(const PrefillArgs& a, const PrefillTile& t, const KeyRan
         load_piece(p + 1);
       }
 #pragma unroll
-      for (int b = 0; b < PB; ++b) {
-        const int h = p * PB + b;
-        const int c = i * HB + h, st = c % kStages;
-        mbar_wait(smem_u32(&empty[st]), (c / kStages + 1) & 1, stop);
-        const uint32_t dst = ring + st * kBlockBytes;
-        const uint32_t* w = raw + b * BW;
-        bool zero = false;
+      for (int x = 0; x < CP; ++x) {
+        const int d = 8 * (p * CP + x), h = d / 64, k = d % 64 / 8;   // eight dims from d: chunk k of block h
+        const int st = (i * HB + h) % kStages;
+        const int un = i * (HB / UB) + h / UB, us = un % (kStages / UB);
+        if (k == 0 && h % UB == 0) mbar_wait(smem_u32(&empty[us]), (un / (kStages / UB) + 1) & 1, stop);
+        const uint32_t* w = raw + x * CW;
+        uint4 y;
         if constexpr (F16) {
-          uint32_t inf = 0;   // a half with all exponent bits set carries into its sign bit
+          if (x == 0) {   // a half with all exponent bits set carries into its sign bit
+            uint32_t inf = 0;
 #pragma unroll
-          for (int x = 0; x < BW; ++x) inf |= ((w[x] & 0x7FFF7FFFu) + 0x04000400u) & 0x80008000u;
-          zero = inf != 0;
-          bad |= zero;
+            for (int v = 0; v < W; ++v) inf |= ((raw[v] & 0x7FFF7FFFu) + 0x04000400u) & 0x80008000u;
+            zero = inf != 0;
+            bad |= zero;
+          }
+          y = zero ? make_uint4(0, 0, 0, 0) : make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+          if (d % 32 == 0) s = make_scale<KIND>(sc[F16 ? 0 : d / 32], bi[AFF ? d / 32 : 0]);
+          y = dequant8<KIND>(w[0], w[CW - 1], s);
         }
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          const int u = F16 ? 0 : (64 * h + 8 * x) / 32;
-          uint4 y;
-          if constexpr (F16)
-            y = zero ? make_uint4(0, 0, 0, 0) : make_uint4(w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
-          else if constexpr (KIND == KVQ_SYM_INT8)
-            y = dequant8<KIND>(w[2 * x], w[2 * x + 1], sc[u], sc[u]);
-          else
-            y = dequant8<KIND>(w[x], 0, sc[u], bi[AFF ? u : 0]);
-          const uint32_t at = dst + ((x ^ (pt & 7)) << 4);
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w)
-                       : "memory");
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(ring + st * kBlockBytes + ((k ^ (pt & 7)) << 4)),
+                     "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w)
+                     : "memory");
+        if (k == 7) {
+          if (F16 && h == HB - 1) publish();   // known only now
+          if ((h + 1) % UB == 0) {
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&full[us]));
+          }
         }
-        if (F16 && h == HB - 1) publish();   // known only now
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&full[st]));
       }
     }
     row1 = row2;
@@ -333,7 +362,7 @@ __device__ __forceinline__ void produce_kind(int kind, const PrefillArgs& a, con
 // The queries of row tile rt, rotated, scaled into fp16 and stored as blocks
 // of 64 dims; HD / 8 lanes share a row.
 template <int HD>
-__device__ void load_queries(const PrefillArgs& a, const PrefillTile& t, int rows, int G, int kvh, int rt, int warp,
+__device__ void load_queries(const PrefillArgs& a, const PrefillTile& t, int rows, int lg, int kvh, int rt, int warp,
                              int lane, Shared<HD>& sh) {
   constexpr int HB = HD / 64, LANES = HD / 8, RPW = 32 / LANES;
   const int li = lane % LANES;
@@ -341,43 +370,61 @@ __device__ void load_queries(const PrefillArgs& a, const PrefillTile& t, int row
   const int order = order_of(a.kl.kind);
   const uint32_t base = smem_u32(sh.q) + rt * HB * kBlockBytes;
   const int d0 = neox ? 4 * li : 8 * li, d1 = neox ? HD / 2 + 4 * li : 8 * li + 4;   // two runs of four
-#pragma unroll 4
-  for (int it = 0; it < 32 / RPW; ++it) {
-    const int r = warp * 32 + it * RPW + lane / LANES, R = rt * 128 + r;
-    float x[8];
+  constexpr int BATCH = 4;   // rows whose loads are in flight together
+#pragma unroll 1
+  for (int it0 = 0; it0 < 32 / RPW; it0 += BATCH) {
+    uint32_t qu[BATCH][4];
+    float4 cs[BATCH][2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = 0.f;
-    if (R < rows) {
-      const int64_t at = ((int64_t)(t.row0 + R / G) * a.n_heads + kvh * G + R % G) * HD;
-      const unsigned short* q = static_cast<const unsigned short*>(a.q) + at;
-      const uint2 u0 = *reinterpret_cast<const uint2*>(q + d0), u1 = *reinterpret_cast<const uint2*>(q + d1);
-      const uint32_t u[4] = {u0.x, u0.y, u1.x, u1.y};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (a.act == KVQ_F16) {
-          const float2 f = __half22float2(u2h(u[i]));
-          x[2 * i] = f.x;
-          x[2 * i + 1] = f.y;
-        } else {
-          x[2 * i] = __uint_as_float(u[i] << 16);
-          x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+    for (int j = 0; j < BATCH; ++j) {
+      const int R = rt * 128 + warp * 32 + (it0 + j) * RPW + lane / LANES;
+      qu[j][0] = qu[j][1] = qu[j][2] = qu[j][3] = 0;
+      cs[j][0] = cs[j][1] = make_float4(1.f, 0.f, 1.f, 0.f);
+      if (R < rows) {
+        const int64_t at = ((int64_t)(t.row0 + (R >> lg)) * a.n_heads + (kvh << lg) + (R & ((1 << lg) - 1))) * HD;
+        const unsigned short* q = static_cast<const unsigned short*>(a.q) + at;
+        const uint2 u0 = *reinterpret_cast<const uint2*>(q + d0), u1 = *reinterpret_cast<const uint2*>(q + d1);
+        qu[j][0] = u0.x;
+        qu[j][1] = u0.y;
+        qu[j][2] = u1.x;
+        qu[j][3] = u1.y;
+        if (a.rope != KVQ_ROPE_NONE) {   // both pairings meet pairs 4 li .. 4 li + 3
+          const float4* c =
+              reinterpret_cast<const float4*>(a.rope_tab + ((int64_t)(t.p0 + (R >> lg)) * (HD / 2) + 4 * li) * 2);
+          cs[j][0] = c[0];
+          cs[j][1] = c[1];
         }
       }
-      if (a.rope != KVQ_ROPE_NONE) {   // both pairings meet pairs 4 li .. 4 li + 3
-        const float4* cs = reinterpret_cast<const float4*>(a.rope_tab + ((int64_t)(t.p0 + R / G) * (HD / 2) + 4 * li) * 2);
-        const float4 c0 = cs[0], c1 = cs[1];
-        const float c[4] = {c0.x, c0.z, c1.x, c1.z}, s[4] = {c0.y, c0.w, c1.y, c1.w};
+    }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float p = neox ? x[i] : x[2 * i], m = neox ? x[4 + i] : x[2 * i + 1];
-          const float y0 = p * c[i] - m * s[i], y1 = p * s[i] + m * c[i];
-          if (neox) {
-            x[i] = y0;
-            x[4 + i] = y1;
-          } else {
-            x[2 * i] = y0;
-            x[2 * i + 1] = y1;
-          }
+    for (int j = 0; j < BATCH; ++j) {
+    const int r = warp * 32 + (it0 + j) * RPW + lane / LANES, R = rt * 128 + r;
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t u = qu[j][i];
+      if (a.act == KVQ_F16) {
+        const float2 f = __half22float2(u2h(u));
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+      } else {
+        x[2 * i] = __uint_as_float(u << 16);
+        x[2 * i + 1] = __uint_as_float(u & 0xFFFF0000u);
+      }
+    }
+    if (a.rope != KVQ_ROPE_NONE) {
+      const float c[4] = {cs[j][0].x, cs[j][0].z, cs[j][1].x, cs[j][1].z};
+      const float s[4] = {cs[j][0].y, cs[j][0].w, cs[j][1].y, cs[j][1].w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float p = neox ? x[i] : x[2 * i], m = neox ? x[4 + i] : x[2 * i + 1];
+        const float y0 = p * c[i] - m * s[i], y1 = p * s[i] + m * c[i];
+        if (neox) {
+          x[i] = y0;
+          x[4 + i] = y1;
+        } else {
+          x[2 * i] = y0;
+          x[2 * i + 1] = y1;
         }
       }
     }
@@ -418,6 +465,7 @@ __device__ void load_queries(const PrefillArgs& a, const PrefillTile& t, int row
                      : "memory");
       }
     }
+    }
   }
 }
 
@@ -448,7 +496,6 @@ struct RowMask {
 template <int HD>
 __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __grid_constant__ PrefillArgs a) {
   constexpr int MT = row_tiles(HD), HB = HD / 64;
-  constexpr int PVN = HD == 256 ? 64 : HD;        // output columns of one product
   constexpr uint32_t kTmemCols = 512;
   extern __shared__ uint8_t raw_smem[];
   Shared<HD>& sh = *reinterpret_cast<Shared<HD>*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~(uintptr_t)1023);
@@ -465,7 +512,10 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
   PrefillTile t;
   if (!find_tile(a, x, kvh == 0 && split == 0 && tid == 0, &t)) return;
   const int rows = t.cnt * G;
-  auto out_row = [&](int r) -> int64_t { return (int64_t)(t.row0 + r / G) * a.n_heads + kvh * G + r % G; };
+  const int lg = 31 - __clz(G);   // G is a power of two
+  auto out_row = [&](int r) -> int64_t {
+    return (int64_t)(t.row0 + (r >> lg)) * a.n_heads + kvh * G + (r & (G - 1));
+  };
   const int64_t ws0 = (int64_t)split * a.n_rows * a.n_heads;
   KeyRange kr = key_range<kKeys>(a, t);
   const int j0 = (int)((int64_t)split * kr.n / a.n_splits), j1 = (int)((int64_t)(split + 1) * kr.n / a.n_splits);
@@ -481,7 +531,7 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
   const int n = j1 - j0;
   const int na = MT == 1 || rows <= 128 ? 1 : 2;   // row tiles with rows
   // Steps of row tile rt: the last ones may lie behind all of its queries.
-  auto last_pos = [&](int rt) { return t.p0 + (min(rows, rt * 128 + 128) - 1) / G; };
+  auto last_pos = [&](int rt) { return t.p0 + ((min(rows, rt * 128 + 128) - 1) >> lg); };
   auto steps = [&](int rt) {
     int k = n;
     while (k > 0 && kr.base<kKeys>(j0 + k - 1) > last_pos(rt)) --k;
@@ -495,8 +545,8 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
     for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_u32(&sh.kfull[i]), 4);
       mbar_init(smem_u32(&sh.vfull[i]), 4);
-      mbar_init(smem_u32(&sh.kempty[i]), 1);
-      mbar_init(smem_u32(&sh.vempty[i]), 1);
+      mbar_init(smem_u32(&sh.kempty[i]), na);   // every row tile is done with it
+      mbar_init(smem_u32(&sh.vempty[i]), na);
     }
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(smem_u32(&sh.kmeta[i]), 4);
@@ -507,8 +557,8 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
       mbar_init(smem_u32(&sh.sfull[i]), 1);
       mbar_init(smem_u32(&sh.pfull[i]), 4);
       mbar_init(smem_u32(&sh.ofull[i]), 1);
+      mbar_init(smem_u32(&sh.drain[i]), 1);
     }
-    mbar_init(smem_u32(&sh.drain), 1);
     sh.stop = 0;
     mbar_init_fence();
   }
@@ -519,15 +569,16 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
 
   if (warp < 4 * MT) {
     // ------------------------------------------------------------ softmax
+    regs_take<regs_softmax(HD)>();
     const int rt = warp >> 2;
     if (rt < na) {
-      load_queries<HD>(a, t, rows, G, kvh, rt, warp & 3, lane, sh);
+      load_queries<HD>(a, t, rows, lg, kvh, rt, warp & 3, lane, sh);
       fence_async_smem();
       group_sync(3 + rt);   // the row scales, written by other lanes
       if (lane == 0) mbar_arrive(smem_u32(&sh.qfull[rt]));
       const int R = rt * 128 + (tid & 127);
-      const int pos = t.p0 + min(R, rows - 1) / G;
-      const int pmin = t.p0 + rt * 128 / G, pmax = last_pos(rt);
+      const int pos = t.p0 + (min(R, rows - 1) >> lg);
+      const int pmin = t.p0 + (rt * 128 >> lg), pmax = last_pos(rt);
       const float qs = sh.qscale[R];
       const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // this warp's 32 lanes of tensor memory
       const uint32_t o_at = tmem + lanes + o_col + rt * HD;
@@ -569,69 +620,60 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
             tc_fence_after();
           }
 #pragma unroll 1
-          for (int d = 0; d < HD; d += 32) {
-            float o[32];
-            tmem_ld32(o_at + d, o);
-            tmem_ld_wait(o);
+          for (int d = 0; d < HD; d += 8) {   // few registers: the scores are live
+            float o[8];
+            tmem_ld8_wait(o_at + d, o);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] *= c;
-            tmem_st32(o_at + d, o);
+            for (int e = 0; e < 8; ++e) o[e] *= c;
+            tmem_st8(o_at + d, o);
           }
         };
         if (ve != held) {   // the same for every row
           if (i > 0) scale_o(pow2i(held - ve));
           held = ve;
         }
-        // One pass over the scores, 32 at a time: P takes the place of S, half
-        // its width, behind the reads.  The running maximum rises, by whole
-        // powers of two, where a row's scores pass it by more than 2^8; what
-        // P the step already has is scaled with O.
-        uint64_t sum = pack2(l, 0.f);
-        const uint64_t f2 = pack2(f, f);
-        float sub = m == -INFINITY ? 0.f : m - kShift;
-#pragma unroll 1
+        // The row's scores, all in registers; P then takes the place of S.
+        float x[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(s_at + 32 * c, x[c]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld_wait(x[c]);
+        if (!whole) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) mask.apply(c, x[c]);
+        }
+        float mc[4];
+#pragma unroll
         for (int c = 0; c < 4; ++c) {
-          float x[32];
-          tmem_ld32(s_at + 32 * c, x);
-          tmem_ld_wait(x);
-          if (!whole) mask.apply(c, x);
-          float mx = fmaxf(x[0], x[1]);
+          mc[c] = fmaxf(x[c][0], x[c][1]);
 #pragma unroll
-          for (int k = 2; k < 32; k += 2) mx = fmaxf(mx, fmaxf(x[k], x[k + 1]));
-          mx *= f;
-          const bool raise = mx > m + kLazy;
-          if (__any_sync(0xffffffffu, raise)) {
-            const float mn = raise ? (m == -INFINITY ? mx : m + ceilf(mx - m)) : m;
-            const float co = raise ? (m == -INFINITY ? 0.f : pow2i((int)(m - mn))) : 1.f;
-            m = mn;
-            sub = m == -INFINITY ? 0.f : m - kShift;
-            const float2 s2 = unpack2(sum);
-            sum = pack2(s2.x * co, s2.y * co);
-            const __half2 c2 = __float2half2_rn(co);
-            tmem_st_wait();   // P written so far is read back
-#pragma unroll 1
-            for (int d = 0; d < c; ++d) {
-              uint32_t w[16];
-              tmem_ld16_wait(s_at + 16 * d, w);
+          for (int k = 2; k < 32; k += 2) mc[c] = fmaxf(mc[c], fmaxf(x[c][k], x[c][k + 1]));
+        }
+        const float mx = fmaxf(fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3])) * f;
+        const bool raise = mx > m + kLazy;
+        if (__any_sync(0xffffffffu, raise)) {
+          const float co = raise ? ex2(m - mx) : 1.f;   // 2^-inf = 0: no key so far
+          if (raise) m = mx;
+          l *= co;
+          if (i > 0) scale_o(co);
+        }
+        const float sub = m == -INFINITY ? 0.f : m - kShift;
+        const uint64_t f2 = pack2(f, f), sub2 = pack2(-sub, -sub);
+        uint64_t sum[2] = {pack2(l, 0.f), pack2(0.f, 0.f)};
 #pragma unroll
-              for (int k = 0; k < 16; ++k) w[k] = h2u(__hmul2(u2h(w[k]), c2));
-              tmem_st16(s_at + 16 * d, w);
-            }
-            if (i > 0) scale_o(co);
-          }
-          const uint64_t sub2 = pack2(-sub, -sub);
+        for (int c = 0; c < 4; ++c) {
           uint32_t w[16];
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
-            const float2 y = unpack2(fma2(pack2(x[2 * k], x[2 * k + 1]), f2, sub2));
+            const float2 y = unpack2(fma2(pack2(x[c][2 * k], x[c][2 * k + 1]), f2, sub2));
             const float p0 = ex2(y.x), p1 = ex2(y.y);
-            sum = add2(sum, pack2(p0, p1));
+            sum[k & 1] = add2(sum[k & 1], pack2(p0, p1));
             w[k] = h2u(__floats2half2_rn(p0, p1));
           }
           tmem_st16(s_at + 16 * c, w);
         }
         {
-          const float2 s2 = unpack2(sum);
+          const float2 s2 = unpack2(add2(sum[0], sum[1]));
           l = s2.x + s2.y;
         }
         tmem_st_wait();
@@ -699,88 +741,96 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
       tc_fence_before();
     }
   } else if (warp < 4 * MT + 4) {
+    regs_give<regs_produce(HD)>();
     produce_kind<HD, false>(a.kl.kind, a, t, kr, j0, n, kvh, tid - 128 * MT, sh, stop);
   } else if (warp < kMmaWarp) {
+    regs_give<regs_produce(HD)>();
     produce_kind<HD, true>(a.vl.kind, a, t, kr, j0, n, kvh, tid - 128 * MT - 128, sh, stop);
   } else {
     // ------------------------------------------------------------ products
-    // The whole warp walks the steps and one lane issues: the descriptors then
-    // stay in uniform registers, where the instruction takes them (a lone lane
-    // in a branch of its own spent 120 cycles on each product, twice its length).
-    const bool leader = elect_one();
-    constexpr uint32_t id_qk = idesc_f16(kKeys, false), id_pv = idesc_f16(PVN, true);
-    // descriptors count addresses in 16 bytes
-    const uint64_t qd = smem_desc(smem_u32(sh.q), 16), kd = smem_desc(smem_u32(sh.k), 16),
-                   vd = smem_desc(smem_u32(sh.v), kBlockBytes);
-    auto wait_full = [&](uint64_t* full, int c) {
-      mbar_wait(smem_u32(&full[c % kStages]), (c / kStages) & 1, stop);
-    };
-    const int nt0 = steps(0), nt1 = na == 2 ? steps(1) : 0;   // nt1 >= nt0: later queries
-    const int lt = na - 1;                                    // the row tile that uses a block last
-    // scores of row tile rt, step i
-    auto qk = [&](int rt, int i) {
-      const int buf = MT == 2 ? rt : i & 1;
-#pragma unroll 1
-      for (int h = 0; h < HB; ++h) {
-        const int c = i * HB + h;
-        wait_full(sh.kfull, c);
-        tc_fence_after();
-        if (leader) {
+    regs_give<kRegsProducts>();   // the whole warpgroup, one warp of which works
+    const int rt = warp - kMmaWarp;
+    if (rt < na) {
+      // A warp issues the products of one row tile, so neither waits for the
+      // other's softmax.  The whole warp walks the steps and one lane issues:
+      // the operands then stay in uniform registers, where the instruction
+      // takes them (a lone lane in a branch of its own spent 120 cycles on each
+      // product, twice its length).
+      constexpr int UB = unit_blocks(HD), NUN = HB / UB, RU = kStages / UB;   // units a step, units a ring
+      constexpr uint32_t id_qk = idesc_f16(kKeys, false), id_pv = idesc_f16(64 * UB, true);
+      // descriptors count addresses in 16 bytes
+      const uint64_t qd = smem_desc(smem_u32(sh.q) + rt * HB * kBlockBytes, 16), kd = smem_desc(smem_u32(sh.k), 16),
+                     vd = smem_desc(smem_u32(sh.v), kBlockBytes);
+      const bool leader = elect_one();
+      const int nt = __shfl_sync(0xffffffffu, steps(rt), 0);
+      const uint32_t s_at = __shfl_sync(0xffffffffu, tmem, 0) + s_col + (MT == 2 ? rt * 128 : 0);
+      const uint32_t o_at = __shfl_sync(0xffffffffu, tmem, 0) + o_col + rt * HD;
+      auto qk = [&](int i) {   // scores of step i
+        const uint32_t s = s_at + (MT == 2 ? 0 : (i & 1) * 128);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          mma_ss(tmem + s_col + buf * 128, qd + ((rt * HB + h) * kBlockBytes + 32 * k) / 16,
-                 kd + ((c % kStages) * kBlockBytes + 32 * k) / 16, id_qk, h > 0 || k > 0);
-        if (rt == lt) mma_commit(smem_u32(&sh.kempty[c % kStages]));
-        if (h == HB - 1) mma_commit(smem_u32(&sh.sfull[buf]));
+        for (int g = 0; g < NUN; ++g) {
+          const int un = i * NUN + g, us = un % RU;
+          mbar_wait(smem_u32(&sh.kfull[us]), (un / RU) & 1, stop);
+          tc_fence_after();
+          if (leader) {
+            const uint64_t b = kd + us * (UB * kBlockBytes / 16);
+#pragma unroll
+            for (int k = 0; k < 4 * UB; ++k)
+              mma_ss(s, qd + ((g * UB + k / 4) * kBlockBytes + 32 * (k % 4)) / 16,
+                     b + ((k / 4) * kBlockBytes + 32 * (k % 4)) / 16, id_qk, g > 0 || k > 0);
+            mma_commit(smem_u32(&sh.kempty[us]));
+            if (g == NUN - 1) mma_commit(smem_u32(&sh.sfull[MT == 2 ? rt : i & 1]));
+          }
+          __syncwarp();
         }
-        __syncwarp();
-      }
-    };
-    // O of row tile rt, step i
-    auto pv = [&](int rt, int i, int nt) {
-      const int buf = MT == 2 ? rt : i & 1;
-      mbar_wait(smem_u32(&sh.pfull[buf]), MT == 2 ? i & 1 : (i >> 1) & 1, stop);
-#pragma unroll 1
-      for (int h = 0; h < HB; h += PVN / 64) {
-        const int c = i * HB + h;
+      };
+      auto pv = [&](int i) {   // O of step i
+        const int buf = MT == 2 ? rt : i & 1;
+        const uint32_t s = s_at + (MT == 2 ? 0 : (i & 1) * 128);
+        mbar_wait(smem_u32(&sh.pfull[buf]), MT == 2 ? i & 1 : (i >> 1) & 1, stop);
 #pragma unroll
-        for (int b = 0; b < PVN / 64; ++b) wait_full(sh.vfull, c + b);
-        tc_fence_after();
-        if (leader) {
+        for (int g = 0; g < NUN; ++g) {
+          const int un = i * NUN + g, us = un % RU;
+          mbar_wait(smem_u32(&sh.vfull[us]), (un / RU) & 1, stop);
+          tc_fence_after();
+          if (leader) {
+            const uint64_t b = vd + us * (UB * kBlockBytes / 16);
 #pragma unroll
-        for (int k = 0; k < kKeys / 16; ++k)
-          mma_ts(tmem + o_col + rt * HD + 64 * h, tmem + s_col + buf * 128 + 8 * k,
-                 vd + ((c % kStages) * kBlockBytes + 2048 * k) / 16, id_pv, i > 0 || k > 0);
-        if (rt == lt) {
-#pragma unroll
-          for (int b = 0; b < PVN / 64; ++b) mma_commit(smem_u32(&sh.vempty[(c + b) % kStages]));
+            for (int k = 0; k < kKeys / 16; ++k)
+              mma_ts(o_at + 64 * UB * g, s + 8 * k, b + 2048 * k / 16, id_pv, i > 0 || k > 0);
+            mma_commit(smem_u32(&sh.vempty[us]));
+            if (g == NUN - 1 && (MT == 1 || i == nt - 1)) mma_commit(smem_u32(&sh.ofull[rt]));
+          }
+          __syncwarp();
         }
-        if (h + PVN / 64 >= HB && (MT == 1 || i == nt - 1)) mma_commit(smem_u32(&sh.ofull[rt]));
-        }
-        __syncwarp();
-      }
-    };
-    for (int rt = 0; rt < na; ++rt) {
+      };
       mbar_wait(smem_u32(&sh.qfull[rt]), 0, stop);
-      if (0 < (rt ? nt1 : nt0)) qk(rt, 0);
-    }
-    for (int i = 0; i < n; ++i) {
-      if constexpr (MT == 1) {
-        if (i + 1 < n) qk(0, i + 1);
-        pv(0, i, n);
-      } else {
+      if (nt > 0) qk(0);
 #pragma unroll 1
-        for (int rt = 0; rt < na; ++rt) {
-          const int nt = rt ? nt1 : nt0;
-          if (i < nt) pv(rt, i, nt);
-          if (i + 1 < nt) qk(rt, i + 1);
+      for (int i = 0; i < nt; ++i) {
+        if (MT == 1 && i + 1 < nt) qk(i + 1);
+        pv(i);
+        if (MT == 2 && i + 1 < nt) qk(i + 1);
+      }
+      // blocks of steps behind this row tile's queries are not waited for
+      for (int i = nt; i < n; ++i) {
+#pragma unroll
+        for (int g = 0; g < NUN; ++g) {
+          const int un = i * NUN + g, us = un % RU;
+          mbar_wait(smem_u32(&sh.kfull[us]), (un / RU) & 1, stop);
+          mbar_wait(smem_u32(&sh.vfull[us]), (un / RU) & 1, stop);
+          if (leader) {
+            mma_commit(smem_u32(&sh.kempty[us]));
+            mma_commit(smem_u32(&sh.vempty[us]));
+          }
+          __syncwarp();
         }
       }
+      if (leader) mma_commit(smem_u32(&sh.drain[rt]));
+      __syncwarp();
+      mbar_wait(smem_u32(&sh.drain[rt]), 0, stop);
+      tc_fence_before();
     }
-    if (leader) mma_commit(smem_u32(&sh.drain));
-    __syncwarp();
-    mbar_wait(smem_u32(&sh.drain), 0, stop);
-    tc_fence_before();
   }
   __syncthreads();
   if (tid == 0 && sh.stop) report(a.status, KVQ_DEV_TIMEOUT);
@@ -794,8 +844,13 @@ template <int HD>
 cudaError_t launch(cudaLaunchConfig_t& lc, const PrefillArgs& a) {
   lc.blockDim = dim3(tc_threads(HD));
   lc.dynamicSmemBytes = shared_bytes<HD>();
-  const cudaError_t e = cudaFuncSetAttribute(prefill_tc_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)shared_bytes<HD>());
+  // the roles' register split counts on the launch's share
+  cudaFuncAttributes at;
+  cudaError_t e = cudaFuncGetAttributes(&at, prefill_tc_kernel<HD>);
+  if (e != cudaSuccess) return e;
+  if (at.numRegs < regs_launch(HD)) return cudaErrorLaunchOutOfResources;
+  e = cudaFuncSetAttribute(prefill_tc_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)shared_bytes<HD>());
   return e != cudaSuccess ? e : cudaLaunchKernelEx(&lc, prefill_tc_kernel<HD>, a);
 }
 

@@ -43,7 +43,8 @@ __device__ __forceinline__ uint64_t now_ns() {
 // Waits for the phase of that parity, two seconds at most; *stop is raised
 // when the time runs out and ends every other wait of the CTA too.
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
-static __device__ __noinline__ void mbar_wait_slow(uint32_t bar, uint32_t parity, volatile int* stop) {
+__device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, volatile int* stop) {
+  if (mbar_try(bar, parity)) return;
   const uint64_t t0 = now_ns();
   while (!mbar_try(bar, parity)) {
     if (*stop) return;
@@ -52,9 +53,6 @@ static __device__ __noinline__ void mbar_wait_slow(uint32_t bar, uint32_t parity
       return;
     }
   }
-}
-__device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, volatile int* stop) {
-  if (!mbar_try(bar, parity)) mbar_wait_slow(bar, parity, stop);
 }
 
 // ---------------------------------------------------------------- pairs of fp32
@@ -79,6 +77,18 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
+}
+
+// ---------------------------------------------------------------- registers
+// A warpgroup's registers a thread, taken from or given back to the block's.
+
+template <int N>
+__device__ __forceinline__ void regs_take() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_give() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // ---------------------------------------------------------------- fences
@@ -123,28 +133,25 @@ __device__ __forceinline__ void tmem_ld_wait(float (&x)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : KVQ_P8(x, 0), KVQ_P8(x, 8), KVQ_P8(x, 16), KVQ_P8(x, 24)::"memory");
 }
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const float (&x)[32]) {
+// Eight columns there and back.
+__device__ __forceinline__ void tmem_ld8_wait(uint32_t addr, float (&x)[8]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
-      "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31};" ::KVQ_F8(x, 0),
-      KVQ_F8(x, 8), KVQ_F8(x, 16), KVQ_F8(x, 24), "r"(addr)
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
+      " tcgen05.wait::ld.sync.aligned;"
+      : KVQ_R8(x, 0)
+      : "r"(addr)
       : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const float (&x)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::KVQ_F8(x, 0),
+               "r"(addr)
+               : "memory");
 }
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t (&x)[16]) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
       "%14, %15};" ::KVQ_I8(x, 0),
       KVQ_I8(x, 8), "r"(addr)
-      : "memory");
-}
-// 16 columns, as words.
-__device__ __forceinline__ void tmem_ld16_wait(uint32_t addr, uint32_t (&x)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15}, [%16];\n tcgen05.wait::ld.sync.aligned;"
-      : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]), "=r"(x[4]), "=r"(x[5]), "=r"(x[6]), "=r"(x[7]), "=r"(x[8]),
-        "=r"(x[9]), "=r"(x[10]), "=r"(x[11]), "=r"(x[12]), "=r"(x[13]), "=r"(x[14]), "=r"(x[15])
-      : "r"(addr)
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
