@@ -77,12 +77,11 @@ constexpr bool split_fits() {
 }
 static_assert(split_fits<64>() && split_fits<128>() && split_fits<256>(), "register split");
 
-// What the softmax needs to know about a step's keys.
+// What the softmax needs to know about the keys of a step, for K and for V.
 struct StepMeta {
-  uint32_t skip[4];   // keys left out (bad pages), a bit each
-  uint32_t bad[4];    // keys that are not finite
-  int e;              // the exponent they are held at
-  int pad[3];
+  int2 head[2];          // the exponent they are held at, and whether any key below is marked
+  uint32_t skip[2][4];   // keys left out (bad pages), a bit each
+  uint32_t bad[2][4];    // keys that are not finite
 };
 
 template <int HD>
@@ -92,12 +91,12 @@ struct Shared {
   uint8_t q[MT * HB * kBlockBytes];
   uint8_t k[kStages * kBlockBytes];
   uint8_t v[kStages * kBlockBytes];
-  StepMeta km[kSlots], vm[kSlots];
+  StepMeta meta[kSlots];
   float qscale[MT * 128];   // f without the keys' part
-  int red[2][2][4];
+  int2 red[2][2][4];
   uint64_t kfull[kStages], kempty[kStages], vfull[kStages], vempty[kStages];   // a unit each
-  uint64_t kmeta[kSlots], vmeta[kSlots];   // a step's metadata are there
-  uint64_t qfull[2], sfull[2], pfull[2];
+  uint64_t ready[kSlots];   // a step's metadata are there
+  uint64_t sfull[2], pfull[2];
   uint64_t ofull[2];   // O of a row tile: its last step (two row tiles), or every step (one)
   uint64_t drain[2];
   uint32_t tmem;
@@ -198,9 +197,9 @@ __device__ void produce(const PrefillArgs& a, const PrefillTile& t, const KeyRan
   const uint32_t ring = smem_u32(IS_V ? sh.v : sh.k) + pt * 128;
   uint64_t* full = IS_V ? sh.vfull : sh.kfull;
   uint64_t* empty = IS_V ? sh.vempty : sh.kempty;
-  uint64_t* ready = IS_V ? sh.vmeta : sh.kmeta;
   const int pb = param_bytes(L.param);
-  const int gu = F16 ? 1 : L.group / 32;     // units a group
+  const int gmask = F16 ? 0 : L.group / 32 - 1;   // units a group (a power of two), less one
+  const int page_bytes = (int)L.page_bytes;       // a page is far below 2 GB
 
   // Row of key pt in step i (-1: none), and its page id (-1 too).
   auto row_at = [&](int i) -> int {
@@ -228,7 +227,7 @@ __device__ void produce(const PrefillArgs& a, const PrefillTile& t, const KeyRan
     nskip = row >= 0 && (page < 0 || page >= a.n_pool_pages);
     if (nskip) report(a.status, KVQ_DEV_BAD_PAGE);
     const bool there = row >= 0 && !nskip;
-    const uint8_t* sub = pool + (there ? page : 0) * L.page_bytes;
+    const uint8_t* sub = pool + (int64_t)(there ? page : 0) * page_bytes;
     src = there ? sub + (row % P) * L.code_bytes : nullptr;
     if constexpr (!F16) {
       const uint8_t* par = sub + P * L.code_bytes + (there ? row % P : 0) * L.param_row_bytes;
@@ -236,16 +235,19 @@ __device__ void produce(const PrefillArgs& a, const PrefillTile& t, const KeyRan
       for (int u = 0; u < NU; ++u) {
         nsc[u] = u ? nsc[u - (u > 0)] : 0.f;
         if constexpr (AFF) nbi[u] = u ? nbi[u - (u > 0)] : 0.f;
-        if (there && u % gu == 0) {
-          const int g = u / gu;
-          nsc[u] = load_param(par + (AFF ? 2 * g : g) * pb, L.param);
-          if constexpr (AFF) nbi[u] = load_param(par + (2 * g + 1) * pb, L.param);
+        if (there && (u & gmask) == 0) {   // parameters follow one another, group by group
+          nsc[u] = load_param(par, L.param);
+          par += pb;
+          if constexpr (AFF) {
+            nbi[u] = load_param(par, L.param);
+            par += pb;
+          }
         }
       }
     }
   };
 
-  int held = IS_V && !F16 ? -100 : 0;   // V: the exponent held so far
+  int held = F16 ? 0 : -100;   // V: the exponent held so far
   int row = row_at(0);
   open_row(row, page_at(row));
   load_piece(0);
@@ -255,10 +257,31 @@ __device__ void produce(const PrefillArgs& a, const PrefillTile& t, const KeyRan
   for (int i = 0; i < n; ++i) {
     const int row2 = row_at(i + 2);
     const int page2 = page_at(row2);
-    StepMeta& meta = (IS_V ? sh.vm : sh.km)[i % kSlots];
+    StepMeta& meta = sh.meta[i % kSlots];
     const bool skip = nskip;
     bool bad = false;
     float sc[NU], bi[AFF ? NU : 1];
+    // Joins the warps' exponents and marks and leaves them for the softmax;
+    // returns the exponent the step is held at (V: the largest so far).
+    auto publish = [&](int e) -> int {
+      const uint32_t ws = __ballot_sync(0xffffffffu, skip), wb = __ballot_sync(0xffffffffu, bad);
+      const int top = __reduce_max_sync(0xffffffffu, e);
+      int2* r = sh.red[IS_V][i & 1];
+      if (lane == 0) {
+        r[warp] = make_int2(top, ws | wb ? 1 : 0);
+        meta.skip[IS_V][warp] = ws;
+        meta.bad[IS_V][warp] = wb;
+      }
+      group_sync(IS_V ? 2 : 1);
+      const int2 r0 = r[0], r1 = r[1], r2 = r[2], r3 = r[3];
+      const int all = max(max(r0.x, r1.x), max(r2.x, r3.x));
+      const int now = IS_V ? max(held, all) : all;
+      if (pt == 0) {
+        meta.head[IS_V] = make_int2(now, r0.y | r1.y | r2.y | r3.y);
+        mbar_arrive(smem_u32(&sh.ready[i % kSlots]));
+      }
+      return now;
+    };
     bool gone = src == nullptr;
     if constexpr (!F16) {
       // the largest scale and bias of the step's keys
@@ -270,13 +293,7 @@ __device__ void produce(const PrefillArgs& a, const PrefillTile& t, const KeyRan
         if constexpr (AFF) mb = fmaxf(mb, fabsf(nbi[u]));
       }
       gone |= bad;
-      const int e1 = gone ? -100 : key_exponent(ms, mb);
-      const int top = __reduce_max_sync(0xffffffffu, e1);
-      if (lane == 0) sh.red[IS_V][i & 1][warp] = top;
-      group_sync(IS_V ? 2 : 1);
-      const int* r = sh.red[IS_V][i & 1];
-      const int e = max(max(r[0], r[1]), max(r[2], r[3]));
-      held = IS_V ? max(held, e) : e;
+      held = publish(gone ? -100 : key_exponent(ms, mb));
       const float down = pow2i(-held);
 #pragma unroll
       for (int u = 0; u < NU; ++u) {
@@ -284,16 +301,6 @@ __device__ void produce(const PrefillArgs& a, const PrefillTile& t, const KeyRan
         if constexpr (AFF) bi[u] = gone ? 0.f : nbi[u] * down;
       }
     }
-    auto publish = [&]() {
-      const uint32_t ws = __ballot_sync(0xffffffffu, skip), wb = __ballot_sync(0xffffffffu, bad);
-      if (lane == 0) {
-        meta.skip[warp] = ws;
-        meta.bad[warp] = wb;
-        if (warp == 0) meta.e = held;
-        mbar_arrive(smem_u32(&ready[i % kSlots]));
-      }
-    };
-    if constexpr (!F16) publish();
     bool zero = false;
     Scale s = {};
 #pragma unroll
@@ -332,7 +339,7 @@ __device__ void produce(const PrefillArgs& a, const PrefillTile& t, const KeyRan
                      "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w)
                      : "memory");
         if (k == 7) {
-          if (F16 && h == HB - 1) publish();   // known only now
+          if (F16 && h == HB - 1) publish(0);   // known only now
           if ((h + 1) % UB == 0) {
             fence_async_smem();
             __syncwarp();
@@ -359,25 +366,25 @@ __device__ __forceinline__ void produce_kind(int kind, const PrefillArgs& a, con
   }
 }
 
-// The queries of row tile rt, rotated, scaled into fp16 and stored as blocks
-// of 64 dims; HD / 8 lanes share a row.
+// The queries of the na row tiles, rotated, scaled into fp16 and stored as
+// blocks of 64 dims; HD / 8 lanes share a row, and every warp of the CTA takes
+// part.
 template <int HD>
-__device__ void load_queries(const PrefillArgs& a, const PrefillTile& t, int rows, int lg, int kvh, int rt, int warp,
+__device__ void load_queries(const PrefillArgs& a, const PrefillTile& t, int rows, int na, int lg, int kvh, int warp,
                              int lane, Shared<HD>& sh) {
-  constexpr int HB = HD / 64, LANES = HD / 8, RPW = 32 / LANES;
+  constexpr int HB = HD / 64, LANES = HD / 8, RPW = 32 / LANES, STEP = tc_threads(HD) / 32 * RPW;
   const int li = lane % LANES;
   const bool neox = a.rope == KVQ_ROPE_NEOX;
   const int order = order_of(a.kl.kind);
-  const uint32_t base = smem_u32(sh.q) + rt * HB * kBlockBytes;
   const int d0 = neox ? 4 * li : 8 * li, d1 = neox ? HD / 2 + 4 * li : 8 * li + 4;   // two runs of four
   constexpr int BATCH = 4;   // rows whose loads are in flight together
 #pragma unroll 1
-  for (int it0 = 0; it0 < 32 / RPW; it0 += BATCH) {
+  for (int r0 = warp * RPW + lane / LANES; r0 < na * 128; r0 += BATCH * STEP) {
     uint32_t qu[BATCH][4];
     float4 cs[BATCH][2];
 #pragma unroll
     for (int j = 0; j < BATCH; ++j) {
-      const int R = rt * 128 + warp * 32 + (it0 + j) * RPW + lane / LANES;
+      const int R = r0 + j * STEP;
       qu[j][0] = qu[j][1] = qu[j][2] = qu[j][3] = 0;
       cs[j][0] = cs[j][1] = make_float4(1.f, 0.f, 1.f, 0.f);
       if (R < rows) {
@@ -398,7 +405,9 @@ __device__ void load_queries(const PrefillArgs& a, const PrefillTile& t, int row
     }
 #pragma unroll
     for (int j = 0; j < BATCH; ++j) {
-    const int r = warp * 32 + (it0 + j) * RPW + lane / LANES, R = rt * 128 + r;
+    const int R = r0 + j * STEP, r = R & 127;
+    if (r0 - lane / LANES + j * STEP >= na * 128) break;   // the same for the whole warp
+    const uint32_t base = smem_u32(sh.q) + (R >> 7) * HB * kBlockBytes;
     float x[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -478,16 +487,16 @@ __device__ __forceinline__ float ex2(float x) {
 // Which of a step's 128 keys a row sees, and which of those are not finite.
 struct RowMask {
   int hi, lo, sinks;   // columns c < hi with c >= lo or c < sinks
-  const uint32_t *skip, *kbad, *vbad;
+  const StepMeta* meta;
   __device__ __forceinline__ uint32_t visible(int c) const {   // columns 32 c .. 32 c + 31
     auto below = [&](int x) -> uint32_t {   // bits of columns < x
       const int k = min(max(x - 32 * c, 0), 32);
       return k == 32 ? ~0u : (1u << k) - 1u;
     };
-    return below(hi) & (~below(lo) | below(sinks)) & ~skip[c];
+    return below(hi) & (~below(lo) | below(sinks)) & ~(meta->skip[0][c] | meta->skip[1][c]);
   }
   __device__ __forceinline__ void apply(int c, float (&x)[32]) const {
-    const uint32_t v = visible(c), b = v & (kbad[c] | vbad[c]);
+    const uint32_t v = visible(c), b = v & (meta->bad[0][c] | meta->bad[1][c]);
 #pragma unroll
     for (int i = 0; i < 32; ++i) x[i] = (b >> i) & 1u ? NAN : ((v >> i) & 1u ? x[i] : -INFINITY);
   }
@@ -549,11 +558,9 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
       mbar_init(smem_u32(&sh.vempty[i]), na);
     }
     for (int i = 0; i < kSlots; ++i) {
-      mbar_init(smem_u32(&sh.kmeta[i]), 4);
-      mbar_init(smem_u32(&sh.vmeta[i]), 4);
+      mbar_init(smem_u32(&sh.ready[i]), 2);   // K's and V's
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&sh.qfull[i]), 4);
       mbar_init(smem_u32(&sh.sfull[i]), 1);
       mbar_init(smem_u32(&sh.pfull[i]), 4);
       mbar_init(smem_u32(&sh.ofull[i]), 1);
@@ -562,6 +569,8 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
     sh.stop = 0;
     mbar_init_fence();
   }
+  load_queries<HD>(a, t, rows, na, lg, kvh, warp, lane, sh);
+  fence_async_smem();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
@@ -572,10 +581,6 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
     regs_take<regs_softmax(HD)>();
     const int rt = warp >> 2;
     if (rt < na) {
-      load_queries<HD>(a, t, rows, lg, kvh, rt, warp & 3, lane, sh);
-      fence_async_smem();
-      group_sync(3 + rt);   // the row scales, written by other lanes
-      if (lane == 0) mbar_arrive(smem_u32(&sh.qfull[rt]));
       const int R = rt * 128 + (tid & 127);
       const int pos = t.p0 + (min(R, rows - 1) >> lg);
       const int pmin = t.p0 + (rt * 128 >> lg), pmax = last_pos(rt);
@@ -588,25 +593,16 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
       for (int i = 0; i < nt; ++i) {
         const int buf = MT == 2 ? rt : i & 1;
         const uint32_t s_at = tmem + lanes + s_col + buf * 128;
-        const StepMeta &km = sh.km[i % kSlots], &vm = sh.vm[i % kSlots];
         // everything but the scores first
-        mbar_wait(smem_u32(&sh.kmeta[i % kSlots]), (i / kSlots) & 1, stop);
-        mbar_wait(smem_u32(&sh.vmeta[i % kSlots]), (i / kSlots) & 1, stop);
-        const float f = fmaxf(qs * pow2i(km.e), 1.17549435e-38f);   // never 0: -inf stays -inf
-        const int ve = vm.e;
+        const StepMeta& meta = sh.meta[i % kSlots];
         const int tb = kr.base<kKeys>(j0 + i), end = kr.end(j0 + i);
-        uint32_t odd = 0;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) odd |= km.skip[c] | km.bad[c] | vm.bad[c];
-        const bool whole = odd == 0 && tb + kKeys <= end && tb + kKeys - 1 <= pmin &&
-                           (a.window == 0 || tb > pmax - a.window || tb + kKeys <= a.sinks);
-        RowMask mask;
-        mask.hi = min(end - tb, pos - tb + 1);
-        mask.lo = a.window == 0 ? 0 : pos - a.window + 1 - tb;
-        mask.sinks = a.window == 0 ? 0 : a.sinks - tb;
-        mask.skip = km.skip;
-        mask.kbad = km.bad;
-        mask.vbad = vm.bad;
+        const bool inside = tb + kKeys <= min(end, pmin + 1) &&
+                            (a.window == 0 || tb > pmax - a.window || tb + kKeys <= a.sinks);
+        mbar_wait(smem_u32(&sh.ready[i % kSlots]), (i / kSlots) & 1, stop);
+        const int4 head = *reinterpret_cast<const int4*>(meta.head);   // K's exponent and marks, V's
+        const float f = fmaxf(qs * pow2i(head.x), 1.17549435e-38f);    // never 0: -inf stays -inf
+        const int ve = head.z;
+        const bool whole = inside && (head.y | head.w) == 0;
         mbar_wait(smem_u32(&sh.sfull[buf]), MT == 2 ? i & 1 : (i >> 1) & 1, stop);
         tc_fence_after();
 
@@ -639,6 +635,11 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld_wait(x[c]);
         if (!whole) {
+          RowMask mask;
+          mask.hi = min(end - tb, pos - tb + 1);
+          mask.lo = a.window == 0 ? 0 : pos - a.window + 1 - tb;
+          mask.sinks = a.window == 0 ? 0 : a.sinks - tb;
+          mask.meta = &meta;
 #pragma unroll
           for (int c = 0; c < 4; ++c) mask.apply(c, x[c]);
         }
@@ -691,8 +692,7 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
       tc_fence_after();
       const bool mine = R < rows;
       const int64_t orow = out_row(mine ? R : 0);
-      const float up = pow2i(held);
-      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const float up = pow2i(held) * (a.n_splits > 1 ? 1.f : (l == 0.f ? 0.f : 1.f / l));
       const int order = order_of(a.vl.kind);
       if (mine && a.n_splits > 1) a.ws_ml[ws0 + orow] = make_float2(m == -INFINITY ? m : m - kShift, l);
 #pragma unroll 1
@@ -720,7 +720,7 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
           uint32_t w[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const float y0 = y[2 * e] * inv * up, y1 = y[2 * e + 1] * inv * up;
+            const float y0 = y[2 * e] * up, y1 = y[2 * e + 1] * up;
             if (a.act == KVQ_F16) {
               w[e] = h2u(__floats2half2_rn(y0, y1));
             } else {
@@ -804,7 +804,6 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
           __syncwarp();
         }
       };
-      mbar_wait(smem_u32(&sh.qfull[rt]), 0, stop);
       if (nt > 0) qk(0);
 #pragma unroll 1
       for (int i = 0; i < nt; ++i) {
