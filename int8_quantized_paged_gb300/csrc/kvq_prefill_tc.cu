@@ -10,9 +10,11 @@
 // Roles, by warp: MT warpgroups of softmax (a thread owns a row: no shuffles),
 // one warpgroup that dequantizes K and one that dequantizes V (a thread owns a
 // key), and a warp that issues the products.  They meet at
-// mbarriers only.  With two row tiles the products of one run while the other's
-// softmax does; head_dim 256 has room for one row tile in tensor memory, so its
-// S is double-buffered instead.
+// mbarriers only.  S comes in halves of 64 keys, two of them in flight per row
+// tile, so that the products of one half run while the softmax works on the
+// other: with a whole step's S in one buffer a row tile's products and softmax
+// took turns.  head_dim 256 has room for one row tile in tensor memory, the
+// others for two.
 //
 // K' and V' sit in shared memory as blocks of 128 keys x 64 dims in the
 // 128-byte swizzle, in two rings of four blocks.  Codes become exact fp16
@@ -51,7 +53,8 @@ namespace {
 
 using namespace um;
 
-constexpr int kKeys = 128;               // keys a step
+constexpr int kKeys = 128;               // keys a step, taken in two halves
+constexpr int kHalf = kKeys / 2;
 constexpr int kStages = 4;               // blocks of a ring
 constexpr int kBlockBytes = kKeys * 128; // 128 keys x 64 dims of fp16
 constexpr int kSlots = 8;                // steps whose metadata are kept
@@ -59,16 +62,16 @@ constexpr float kLazy = 8.0f;            // the running maximum rises past +2^8 
 constexpr float kShift = 7.0f;           // P is held times 2^7
 
 __host__ __device__ constexpr int row_tiles(int hd) { return hd == 256 ? 1 : 2; }
-// Blocks that change hands together: a whole step's, or at head_dim 256, where
-// the ring holds one step only, one.
+// Blocks that change hands together, half their keys at a time: a whole step's,
+// or at head_dim 256, where the ring holds one step only, one.
 __host__ __device__ constexpr int unit_blocks(int hd) { return hd == 256 ? 1 : hd / 64; }
 __host__ __device__ constexpr int tc_threads(int hd) { return 128 * row_tiles(hd) + 256 + 128; }
 // Registers a thread: at launch (65536 over the threads, in eights), then by
 // role.  A role may only take what the others gave back, so the shares must
 // not exceed the launch's: (softmax * tiles + 2 producers + products) * 128.
 __host__ __device__ constexpr int regs_launch(int hd) { return 65536 / tc_threads(hd) / 8 * 8; }
-__host__ __device__ constexpr int regs_softmax(int hd) { return hd == 256 ? 208 : 152; }
-__host__ __device__ constexpr int regs_produce(int hd) { return hd == 256 ? 120 : 72; }
+__host__ __device__ constexpr int regs_softmax(int hd) { return hd == 256 ? 184 : 136; }
+__host__ __device__ constexpr int regs_produce(int hd) { return hd == 256 ? 128 : 88; }
 constexpr int kRegsProducts = 32;
 template <int HD>
 constexpr bool split_fits() {
@@ -94,11 +97,12 @@ struct Shared {
   StepMeta meta[kSlots];
   float qscale[MT * 128];   // f without the keys' part
   int2 red[2][2][4];
-  uint64_t kfull[kStages], kempty[kStages], vfull[kStages], vempty[kStages];   // a unit each
+  // half a unit each
+  uint64_t kfull[kStages][2], kempty[kStages][2], vfull[kStages][2], vempty[kStages][2];
   uint64_t ready[kSlots];   // a step's metadata are there
-  uint64_t sfull[2], pfull[2];
-  uint64_t ofull[2];   // O of a row tile: its last step (two row tiles), or every step (one)
-  uint64_t drain[2];
+  uint64_t sfull[MT][2], pfull[MT][2];   // scores and weights of a half step
+  uint64_t ofull[MT];                    // O of a row tile, every half step
+  uint64_t drain[MT];
   uint32_t tmem;
   int stop;
 };
@@ -195,8 +199,9 @@ __device__ void produce(const PrefillArgs& a, const PrefillTile& t, const KeyRan
   const int32_t* bt = a.block_table + (int64_t)t.b * a.max_pages;
   const int warp = pt >> 5, lane = pt & 31;
   const uint32_t ring = smem_u32(IS_V ? sh.v : sh.k) + pt * 128;
-  uint64_t* full = IS_V ? sh.vfull : sh.kfull;
-  uint64_t* empty = IS_V ? sh.vempty : sh.kempty;
+  uint64_t(*full)[2] = IS_V ? sh.vfull : sh.kfull;
+  uint64_t(*empty)[2] = IS_V ? sh.vempty : sh.kempty;
+  const int kh = pt / kHalf;   // its half of the step
   const int pb = param_bytes(L.param);
   const int gmask = F16 ? 0 : L.group / 32 - 1;   // units a group (a power of two), less one
   const int page_bytes = (int)L.page_bytes;       // a page is far below 2 GB
@@ -319,7 +324,7 @@ __device__ void produce(const PrefillArgs& a, const PrefillTile& t, const KeyRan
         const int d = 8 * (p * CP + x), h = d / 64, k = d % 64 / 8;   // eight dims from d: chunk k of block h
         const int st = (i * HB + h) % kStages;
         const int un = i * (HB / UB) + h / UB, us = un % (kStages / UB);
-        if (k == 0 && h % UB == 0) mbar_wait(smem_u32(&empty[us]), (un / (kStages / UB) + 1) & 1, stop);
+        if (k == 0 && h % UB == 0) mbar_wait(smem_u32(&empty[us][kh]), (un / (kStages / UB) + 1) & 1, stop);
         const uint32_t* w = raw + x * CW;
         uint4 y;
         if constexpr (F16) {
@@ -343,7 +348,7 @@ __device__ void produce(const PrefillArgs& a, const PrefillTile& t, const KeyRan
           if ((h + 1) % UB == 0) {
             fence_async_smem();
             __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&full[us]));
+            if (lane == 0) mbar_arrive(smem_u32(&full[us][kh]));
           }
         }
       }
@@ -498,7 +503,11 @@ struct RowMask {
   __device__ __forceinline__ void apply(int c, float (&x)[32]) const {
     const uint32_t v = visible(c), b = v & (meta->bad[0][c] | meta->bad[1][c]);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) x[i] = (b >> i) & 1u ? NAN : ((v >> i) & 1u ? x[i] : -INFINITY);
+    for (int i = 0; i < 32; ++i) x[i] = (v >> i) & 1u ? x[i] : -INFINITY;
+    if (__any_sync(0xffffffffu, b != 0)) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) x[i] = (b >> i) & 1u ? NAN : x[i];
+    }
   }
 };
 
@@ -539,11 +548,11 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
   }
   const int n = j1 - j0;
   const int na = MT == 1 || rows <= 128 ? 1 : 2;   // row tiles with rows
-  // Steps of row tile rt: the last ones may lie behind all of its queries.
+  // Half steps of row tile rt: the last ones may lie behind all of its queries.
   auto last_pos = [&](int rt) { return t.p0 + ((min(rows, rt * 128 + 128) - 1) >> lg); };
-  auto steps = [&](int rt) {
-    int k = n;
-    while (k > 0 && kr.base<kKeys>(j0 + k - 1) > last_pos(rt)) --k;
+  auto half_steps = [&](int rt) {
+    int k = 2 * n;
+    while (k > 0 && kr.base<kKeys>(j0 + (k - 1) / 2) + (k - 1) % 2 * kHalf > last_pos(rt)) --k;
     return k;
   };
 
@@ -551,18 +560,20 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
   if (warp == kMmaWarp) {
     tmem_alloc(smem_u32(&sh.tmem), kTmemCols);
   } else if (tid == 0) {
-    for (int i = 0; i < kStages; ++i) {
-      mbar_init(smem_u32(&sh.kfull[i]), 4);
-      mbar_init(smem_u32(&sh.vfull[i]), 4);
-      mbar_init(smem_u32(&sh.kempty[i]), na);   // every row tile is done with it
-      mbar_init(smem_u32(&sh.vempty[i]), na);
+    for (int i = 0; i < kStages * 2; ++i) {
+      mbar_init(smem_u32(&sh.kfull[0][0] + i), 2);
+      mbar_init(smem_u32(&sh.vfull[0][0] + i), 2);
+      mbar_init(smem_u32(&sh.kempty[0][0] + i), na);   // every row tile is done with it
+      mbar_init(smem_u32(&sh.vempty[0][0] + i), na);
     }
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(smem_u32(&sh.ready[i]), 2);   // K's and V's
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(smem_u32(&sh.sfull[i]), 1);
-      mbar_init(smem_u32(&sh.pfull[i]), 4);
+    for (int i = 0; i < MT; ++i) {
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(smem_u32(&sh.sfull[i][h]), 1);
+        mbar_init(smem_u32(&sh.pfull[i][h]), 4);
+      }
       mbar_init(smem_u32(&sh.ofull[i]), 1);
       mbar_init(smem_u32(&sh.drain[i]), 1);
     }
@@ -578,7 +589,7 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
 
   if (warp < 4 * MT) {
     // ------------------------------------------------------------ softmax
-    regs_take<regs_softmax(HD)>();
+    regs_set<regs_softmax(HD), regs_launch(HD)>();
     const int rt = warp >> 2;
     if (rt < na) {
       const int R = rt * 128 + (tid & 127);
@@ -587,34 +598,36 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
       const float qs = sh.qscale[R];
       const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // this warp's 32 lanes of tensor memory
       const uint32_t o_at = tmem + lanes + o_col + rt * HD;
-      const int nt = steps(rt);
-      float m = -INFINITY, l = 0.f;
-      int held = 0;
-      for (int i = 0; i < nt; ++i) {
-        const int buf = MT == 2 ? rt : i & 1;
-        const uint32_t s_at = tmem + lanes + s_col + buf * 128;
-        // everything but the scores first
+      const int nh = half_steps(rt);
+      float m = -INFINITY, l = 0.f, f = 0.f;
+      int held = 0, tb = 0, end = 0, ve = 0;
+      bool whole = false;
+#pragma unroll 1
+      for (int u = 0; u < nh; ++u) {
+        const int i = u >> 1, hf = u & 1;
+        const uint32_t s_at = tmem + lanes + s_col + rt * 128 + hf * 64;
         const StepMeta& meta = sh.meta[i % kSlots];
-        const int tb = kr.base<kKeys>(j0 + i), end = kr.end(j0 + i);
-        const bool inside = tb + kKeys <= min(end, pmin + 1) &&
-                            (a.window == 0 || tb > pmax - a.window || tb + kKeys <= a.sinks);
-        mbar_wait(smem_u32(&sh.ready[i % kSlots]), (i / kSlots) & 1, stop);
-        const int4 head = *reinterpret_cast<const int4*>(meta.head);   // K's exponent and marks, V's
-        const float f = fmaxf(qs * pow2i(head.x), 1.17549435e-38f);    // never 0: -inf stays -inf
-        const int ve = head.z;
-        const bool whole = inside && (head.y | head.w) == 0;
-        mbar_wait(smem_u32(&sh.sfull[buf]), MT == 2 ? i & 1 : (i >> 1) & 1, stop);
+        if (hf == 0) {   // everything but the scores first
+          tb = kr.base<kKeys>(j0 + i);
+          end = kr.end(j0 + i);
+          const bool inside = tb + kKeys <= min(end, pmin + 1) &&
+                              (a.window == 0 || tb > pmax - a.window || tb + kKeys <= a.sinks);
+          mbar_wait(smem_u32(&sh.ready[i % kSlots]), (i / kSlots) & 1, stop);
+          const int4 head = *reinterpret_cast<const int4*>(meta.head);   // K's exponent and marks, V's
+          f = fmaxf(qs * pow2i(head.x), 1.17549435e-38f);                // never 0: -inf stays -inf
+          ve = head.z;
+          whole = inside && (head.y | head.w) == 0;
+        }
+        mbar_wait(smem_u32(&sh.sfull[rt][hf]), i & 1, stop);
         tc_fence_after();
 
         // O of the steps before, times a power of two a row.
         auto scale_o = [&](float c) {
-          // O is at rest: with two row tiles this step's scores were issued
-          // after the last step's O; with one, they were issued before it, but
-          // after that of the step before, so the parity is not ambiguous
-          if constexpr (MT == 1) {
-            mbar_wait(smem_u32(&sh.ofull[0]), (i - 1) & 1, stop);
-            tc_fence_after();
-          }
+          // O is at rest once the last half step's product is done.  This one's
+          // scores were issued after the product of the one before that, so the
+          // parity is not ambiguous.
+          mbar_wait(smem_u32(&sh.ofull[rt]), (u - 1) & 1, stop);
+          tc_fence_after();
 #pragma unroll 1
           for (int d = 0; d < HD; d += 8) {   // few registers: the scores are live
             float o[8];
@@ -625,15 +638,15 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
           }
         };
         if (ve != held) {   // the same for every row
-          if (i > 0) scale_o(pow2i(held - ve));
+          if (u > 0) scale_o(pow2i(held - ve));
           held = ve;
         }
-        // The row's scores, all in registers; P then takes the place of S.
-        float x[4][32];
+        // The row's 64 scores, all in registers; P then takes the place of S.
+        float x[2][32];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(s_at + 32 * c, x[c]);
+        for (int c = 0; c < 2; ++c) tmem_ld32(s_at + 32 * c, x[c]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld_wait(x[c]);
+        for (int c = 0; c < 2; ++c) tmem_ld_wait(x[c]);
         if (!whole) {
           RowMask mask;
           mask.hi = min(end - tb, pos - tb + 1);
@@ -641,28 +654,28 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
           mask.sinks = a.window == 0 ? 0 : a.sinks - tb;
           mask.meta = &meta;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) mask.apply(c, x[c]);
+          for (int c = 0; c < 2; ++c) mask.apply(2 * hf + c, x[c]);
         }
         float mc[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          mc[c] = fmaxf(x[c][0], x[c][1]);
+        for (int e = 0; e < 4; ++e) mc[e] = fmaxf(x[0][e], x[0][e + 4]);
 #pragma unroll
-          for (int k = 2; k < 32; k += 2) mc[c] = fmaxf(mc[c], fmaxf(x[c][k], x[c][k + 1]));
-        }
+        for (int k = 8; k < 64; k += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mc[e] = fmaxf(mc[e], fmaxf(x[k / 32][k % 32 + e], x[k / 32][k % 32 + 4 + e]));
         const float mx = fmaxf(fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3])) * f;
         const bool raise = mx > m + kLazy;
         if (__any_sync(0xffffffffu, raise)) {
           const float co = raise ? ex2(m - mx) : 1.f;   // 2^-inf = 0: no key so far
           if (raise) m = mx;
           l *= co;
-          if (i > 0) scale_o(co);
+          if (u > 0) scale_o(co);
         }
         const float sub = m == -INFINITY ? 0.f : m - kShift;
         const uint64_t f2 = pack2(f, f), sub2 = pack2(-sub, -sub);
         uint64_t sum[2] = {pack2(l, 0.f), pack2(0.f, 0.f)};
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 2; ++c) {
           uint32_t w[16];
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
@@ -680,15 +693,11 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sh.pfull[buf]));
+        if (lane == 0) mbar_arrive(smem_u32(&sh.pfull[rt][hf]));
       }
       // ---- the result: O 2^held / l, dims back in order
-      if constexpr (MT == 1) {
-        if (nt > 1) mbar_wait(smem_u32(&sh.ofull[0]), (nt - 2) & 1, stop);
-        mbar_wait(smem_u32(&sh.ofull[0]), (nt - 1) & 1, stop);
-      } else if (nt > 0) {
-        mbar_wait(smem_u32(&sh.ofull[rt]), 0, stop);
-      }
+      if (nh > 1) mbar_wait(smem_u32(&sh.ofull[rt]), (nh - 2) & 1, stop);
+      if (nh > 0) mbar_wait(smem_u32(&sh.ofull[rt]), (nh - 1) & 1, stop);
       tc_fence_after();
       const bool mine = R < rows;
       const int64_t orow = out_row(mine ? R : 0);
@@ -698,7 +707,7 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
 #pragma unroll 1
       for (int d = 0; d < HD; d += 32) {
         float o[32], y[32];
-        if (nt > 0) {
+        if (nh > 0) {
           tmem_ld32(o_at + d, o);
           tmem_ld_wait(o);
         } else {
@@ -741,14 +750,14 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
       tc_fence_before();
     }
   } else if (warp < 4 * MT + 4) {
-    regs_give<regs_produce(HD)>();
+    regs_set<regs_produce(HD), regs_launch(HD)>();
     produce_kind<HD, false>(a.kl.kind, a, t, kr, j0, n, kvh, tid - 128 * MT, sh, stop);
   } else if (warp < kMmaWarp) {
-    regs_give<regs_produce(HD)>();
+    regs_set<regs_produce(HD), regs_launch(HD)>();
     produce_kind<HD, true>(a.vl.kind, a, t, kr, j0, n, kvh, tid - 128 * MT - 128, sh, stop);
   } else {
     // ------------------------------------------------------------ products
-    regs_give<kRegsProducts>();   // the whole warpgroup, one warp of which works
+    regs_set<kRegsProducts, regs_launch(HD)>();   // the whole warpgroup, one warp of which works
     const int rt = warp - kMmaWarp;
     if (rt < na) {
       // A warp issues the products of one row tile, so neither waits for the
@@ -757,70 +766,73 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
       // takes them (a lone lane in a branch of its own spent 120 cycles on each
       // product, twice its length).
       constexpr int UB = unit_blocks(HD), NUN = HB / UB, RU = kStages / UB;   // units a step, units a ring
-      constexpr uint32_t id_qk = idesc_f16(kKeys, false), id_pv = idesc_f16(64 * UB, true);
+      constexpr uint32_t id_qk = idesc_f16(kHalf, false), id_pv = idesc_f16(64 * UB, true);
+      constexpr int kHalfBytes = kHalf * 128;   // half the keys of a block
       // descriptors count addresses in 16 bytes
       const uint64_t qd = smem_desc(smem_u32(sh.q) + rt * HB * kBlockBytes, 16), kd = smem_desc(smem_u32(sh.k), 16),
                      vd = smem_desc(smem_u32(sh.v), kBlockBytes);
       const bool leader = elect_one();
-      const int nt = __shfl_sync(0xffffffffu, steps(rt), 0);
-      const uint32_t s_at = __shfl_sync(0xffffffffu, tmem, 0) + s_col + (MT == 2 ? rt * 128 : 0);
+      const int nh = __shfl_sync(0xffffffffu, half_steps(rt), 0);
+      const uint32_t s_at = __shfl_sync(0xffffffffu, tmem, 0) + s_col + rt * 128;
       const uint32_t o_at = __shfl_sync(0xffffffffu, tmem, 0) + o_col + rt * HD;
-      auto qk = [&](int i) {   // scores of step i
-        const uint32_t s = s_at + (MT == 2 ? 0 : (i & 1) * 128);
+      auto qk = [&](int u) {   // scores of half step u
+        const int i = u >> 1, hf = u & 1;
 #pragma unroll
         for (int g = 0; g < NUN; ++g) {
           const int un = i * NUN + g, us = un % RU;
-          mbar_wait(smem_u32(&sh.kfull[us]), (un / RU) & 1, stop);
+          mbar_wait(smem_u32(&sh.kfull[us][hf]), (un / RU) & 1, stop);
           tc_fence_after();
           if (leader) {
-            const uint64_t b = kd + us * (UB * kBlockBytes / 16);
+            const uint64_t b = kd + (us * UB * kBlockBytes + hf * kHalfBytes) / 16;
 #pragma unroll
             for (int k = 0; k < 4 * UB; ++k)
-              mma_ss(s, qd + ((g * UB + k / 4) * kBlockBytes + 32 * (k % 4)) / 16,
+              mma_ss(s_at + hf * 64, qd + ((g * UB + k / 4) * kBlockBytes + 32 * (k % 4)) / 16,
                      b + ((k / 4) * kBlockBytes + 32 * (k % 4)) / 16, id_qk, g > 0 || k > 0);
-            mma_commit(smem_u32(&sh.kempty[us]));
-            if (g == NUN - 1) mma_commit(smem_u32(&sh.sfull[MT == 2 ? rt : i & 1]));
+            mma_commit(smem_u32(&sh.kempty[us][hf]));
+            if (g == NUN - 1) mma_commit(smem_u32(&sh.sfull[rt][hf]));
           }
           __syncwarp();
         }
       };
-      auto pv = [&](int i) {   // O of step i
-        const int buf = MT == 2 ? rt : i & 1;
-        const uint32_t s = s_at + (MT == 2 ? 0 : (i & 1) * 128);
-        mbar_wait(smem_u32(&sh.pfull[buf]), MT == 2 ? i & 1 : (i >> 1) & 1, stop);
+      auto pv = [&](int u) {   // O of half step u
+        const int i = u >> 1, hf = u & 1;
+        mbar_wait(smem_u32(&sh.pfull[rt][hf]), i & 1, stop);
 #pragma unroll
         for (int g = 0; g < NUN; ++g) {
           const int un = i * NUN + g, us = un % RU;
-          mbar_wait(smem_u32(&sh.vfull[us]), (un / RU) & 1, stop);
+          mbar_wait(smem_u32(&sh.vfull[us][hf]), (un / RU) & 1, stop);
           tc_fence_after();
           if (leader) {
-            const uint64_t b = vd + us * (UB * kBlockBytes / 16);
+            const uint64_t b = vd + (us * UB * kBlockBytes + hf * kHalfBytes) / 16;
 #pragma unroll
-            for (int k = 0; k < kKeys / 16; ++k)
-              mma_ts(o_at + 64 * UB * g, s + 8 * k, b + 2048 * k / 16, id_pv, i > 0 || k > 0);
-            mma_commit(smem_u32(&sh.vempty[us]));
-            if (g == NUN - 1 && (MT == 1 || i == nt - 1)) mma_commit(smem_u32(&sh.ofull[rt]));
+            for (int k = 0; k < kHalf / 16; ++k)
+              mma_ts(o_at + 64 * UB * g, s_at + hf * 64 + 8 * k, b + 2048 * k / 16, id_pv, u > 0 || k > 0);
+            mma_commit(smem_u32(&sh.vempty[us][hf]));
+            if (g == NUN - 1) mma_commit(smem_u32(&sh.ofull[rt]));
           }
           __syncwarp();
         }
       };
-      if (nt > 0) qk(0);
+      // Scores run two half steps ahead of the weights, in two buffers.
+      if (nh > 0) qk(0);
+      if (nh > 1) qk(1);
 #pragma unroll 1
-      for (int i = 0; i < nt; ++i) {
-        if (MT == 1 && i + 1 < nt) qk(i + 1);
-        pv(i);
-        if (MT == 2 && i + 1 < nt) qk(i + 1);
+      for (int u = 0; u < nh; ++u) {
+        pv(u);
+        if (u + 2 < nh) qk(u + 2);
       }
-      // blocks of steps behind this row tile's queries are not waited for
-      for (int i = nt; i < n; ++i) {
+      // blocks behind this row tile's queries are given back unread
+#pragma unroll 1
+      for (int u = nh; u < 2 * n; ++u) {
+        const int i = u >> 1, hf = u & 1;
 #pragma unroll
         for (int g = 0; g < NUN; ++g) {
           const int un = i * NUN + g, us = un % RU;
-          mbar_wait(smem_u32(&sh.kfull[us]), (un / RU) & 1, stop);
-          mbar_wait(smem_u32(&sh.vfull[us]), (un / RU) & 1, stop);
+          mbar_wait(smem_u32(&sh.kfull[us][hf]), (un / RU) & 1, stop);
+          mbar_wait(smem_u32(&sh.vfull[us][hf]), (un / RU) & 1, stop);
           if (leader) {
-            mma_commit(smem_u32(&sh.kempty[us]));
-            mma_commit(smem_u32(&sh.vempty[us]));
+            mma_commit(smem_u32(&sh.kempty[us][hf]));
+            mma_commit(smem_u32(&sh.vempty[us][hf]));
           }
           __syncwarp();
         }

@@ -80,15 +80,14 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 }
 
 // ---------------------------------------------------------------- registers
-// A warpgroup's registers a thread, taken from or given back to the block's.
-
-template <int N>
-__device__ __forceinline__ void regs_take() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_give() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+// Sets a warpgroup's registers a thread to N, of FROM at launch: more are taken
+// from what others gave back (the instruction waits for them), fewer are given
+// back.  Each direction has its own instruction, and the other is illegal.
+template <int N, int FROM>
+__device__ __forceinline__ void regs_set() {
+  static_assert(N % 8 == 0 && N >= 24 && N <= 256, "registers a thread");
+  if constexpr (N > FROM) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+  if constexpr (N < FROM) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // ---------------------------------------------------------------- fences
