@@ -101,7 +101,7 @@ struct Shared {
   uint64_t kfull[kStages][2], kempty[kStages][2], vfull[kStages][2], vempty[kStages][2];
   uint64_t ready[kSlots];   // a step's metadata are there
   uint64_t sfull[MT][2], pfull[MT][2];   // scores and weights of a half step
-  uint64_t ofull[MT];                    // O of a row tile, every half step
+  uint64_t ofull[MT][2];                 // O with it
   uint64_t drain[MT];
   uint32_t tmem;
   int stop;
@@ -122,7 +122,10 @@ __device__ __forceinline__ int key_exponent(float s, float b) {
   return max(max(exponent_of(s) + 9, exponent_of(b) - 14), -100);
 }
 constexpr float kMostScale = 1.0e35f;   // held at 2^126 at most: a larger scale counts as not finite
-__device__ __forceinline__ void group_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ void group_sync(int id) {
+  __syncwarp();
+  asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory");
+}
 
 __device__ __forceinline__ uint32_t h2u(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 __device__ __forceinline__ __half2 u2h(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
@@ -573,8 +576,8 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
       for (int h = 0; h < 2; ++h) {
         mbar_init(smem_u32(&sh.sfull[i][h]), 1);
         mbar_init(smem_u32(&sh.pfull[i][h]), 4);
+        mbar_init(smem_u32(&sh.ofull[i][h]), 1);
       }
-      mbar_init(smem_u32(&sh.ofull[i]), 1);
       mbar_init(smem_u32(&sh.drain[i]), 1);
     }
     sh.stop = 0;
@@ -623,10 +626,11 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
 
         // O of the steps before, times a power of two a row.
         auto scale_o = [&](float c) {
-          // O is at rest once the last half step's product is done.  This one's
-          // scores were issued after the product of the one before that, so the
-          // parity is not ambiguous.
-          mbar_wait(smem_u32(&sh.ofull[rt]), (u - 1) & 1, stop);
+          // O is at rest once the last half step's product is done.  A barrier
+          // for even and one for odd half steps: the phase before the awaited
+          // one is product u - 3, done before scores u - 1 were, and the phase
+          // behind it needs this row's weights, so the parity says which.
+          mbar_wait(smem_u32(&sh.ofull[rt][hf ^ 1]), ((u - 1) >> 1) & 1, stop);
           tc_fence_after();
 #pragma unroll 1
           for (int d = 0; d < HD; d += 8) {   // few registers: the scores are live
@@ -696,8 +700,7 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
         if (lane == 0) mbar_arrive(smem_u32(&sh.pfull[rt][hf]));
       }
       // ---- the result: O 2^held / l, dims back in order
-      if (nh > 1) mbar_wait(smem_u32(&sh.ofull[rt]), (nh - 2) & 1, stop);
-      if (nh > 0) mbar_wait(smem_u32(&sh.ofull[rt]), (nh - 1) & 1, stop);
+      if (nh > 0) mbar_wait(smem_u32(&sh.ofull[rt][(nh - 1) & 1]), ((nh - 1) >> 1) & 1, stop);
       tc_fence_after();
       const bool mine = R < rows;
       const int64_t orow = out_row(mine ? R : 0);
@@ -808,7 +811,7 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
             for (int k = 0; k < kHalf / 16; ++k)
               mma_ts(o_at + 64 * UB * g, s_at + hf * 64 + 8 * k, b + 2048 * k / 16, id_pv, u > 0 || k > 0);
             mma_commit(smem_u32(&sh.vempty[us][hf]));
-            if (g == NUN - 1) mma_commit(smem_u32(&sh.ofull[rt]));
+            if (g == NUN - 1) mma_commit(smem_u32(&sh.ofull[rt][hf]));
           }
           __syncwarp();
         }

@@ -43,16 +43,15 @@ __device__ __forceinline__ uint64_t now_ns() {
 // Waits for the phase of that parity, two seconds at most; *stop is raised
 // when the time runs out and ends every other wait of the CTA too.
 constexpr uint64_t kWaitLimitNs = 2000000000ull;
+// A whole warp calls it, and leaves it converged, as the .aligned instructions
+// behind it need.
 __device__ __forceinline__ void mbar_wait(uint32_t bar, uint32_t parity, volatile int* stop) {
-  if (mbar_try(bar, parity)) return;
-  const uint64_t t0 = now_ns();
-  while (!mbar_try(bar, parity)) {
-    if (*stop) return;
-    if (now_ns() - t0 > kWaitLimitNs) {
-      *stop = 1;
-      return;
-    }
+  if (!mbar_try(bar, parity)) {
+    const uint64_t t0 = now_ns();
+    while (!mbar_try(bar, parity) && !*stop)
+      if (now_ns() - t0 > kWaitLimitNs) *stop = 1;
   }
+  __syncwarp();
 }
 
 // ---------------------------------------------------------------- pairs of fp32

@@ -340,6 +340,23 @@ def test_streams_and_graphs():
     c.close()
 
 
+@pytest.mark.parametrize("key", ["llama8b", "llama8b_f16", "gemma", "tiny_f16"])
+def test_calls_back_to_back(key):
+    """Many calls with nothing between them: no wait inside the kernel runs out, and every call gives the same bits."""
+    c = Cache(layer(key), [1500, 700, 64])
+    news = [700, 699, 64]
+    q = c.queries(sum(news))
+    want = _prefill(c, q, news)
+    lens = torch.tensor(c.lens, dtype=torch.int32, device="cuda")
+    st, out, ws = _starts(news), torch.empty_like(q), c.c.prefill_workspace(3, len(q))
+    for _ in range(8):
+        for _ in range(40):
+            c.c.prefill(q, st, lens, out, ws)
+        assert c.c.status_bits() == 0
+        assert torch.equal(out, want)
+    c.close()
+
+
 @pytest.mark.parametrize("key", ["llama8b", "gemma_bf16", "tiny"])
 def test_a_session(key):
     """As a server runs it: a prompt through a pinned ring in chunks, each appended and
