@@ -100,6 +100,7 @@ struct Shared {
   // half a unit each
   uint64_t kfull[kStages][2], kempty[kStages][2], vfull[kStages][2], vempty[kStages][2];
   uint64_t ready[kSlots];   // a step's metadata are there
+  uint64_t qfull;                        // the queries are there
   uint64_t sfull[MT][2], pfull[MT][2];   // scores and weights of a half step
   uint64_t ofull[MT][2];                 // O with it
   uint64_t drain[MT];
@@ -201,7 +202,8 @@ __device__ void produce(const PrefillArgs& a, const PrefillTile& t, const KeyRan
   const uint8_t* pool = (IS_V ? a.v_pool : a.k_pool) + (int64_t)kvh * L.sub_bytes;
   const int32_t* bt = a.block_table + (int64_t)t.b * a.max_pages;
   const int warp = pt >> 5, lane = pt & 31;
-  const uint32_t ring = smem_u32(IS_V ? sh.v : sh.k) + pt * 128;
+  // its row of a block, and there the chunk that chunk 0 is stored at
+  const uint32_t ring = smem_u32(IS_V ? sh.v : sh.k) + pt * 128 + ((pt & 7) << 4);
   uint64_t(*full)[2] = IS_V ? sh.vfull : sh.kfull;
   uint64_t(*empty)[2] = IS_V ? sh.vempty : sh.kempty;
   const int kh = pt / kHalf;   // its half of the step
@@ -216,29 +218,31 @@ __device__ void produce(const PrefillArgs& a, const PrefillTile& t, const KeyRan
     return key < kr.end(j0 + i) ? row_of(key, a.ring_rows, a.pin_rows) : -1;
   };
   auto page_at = [&](int row) -> int { return row >= 0 ? bt[row / P] : -1; };
-  uint32_t nraw[W];
+  uint32_t raw[W];
   float nsc[NU], nbi[AFF ? NU : 1];
-  const uint8_t* src = nullptr;   // codes of the row being loaded; null: no such row
-  bool nskip = false;
+  const uint8_t* src = pool;        // codes of the row being loaded
+  bool nthere = false, nskip = false;   // whether there is one; whether its page is bad
   auto load_piece = [&](int p) {
     const uint4* s = reinterpret_cast<const uint4*>(src + p * (4 * W));
 #pragma unroll
     for (int x = 0; x < W / 4; ++x) {
-      const uint4 y = src ? __ldg(s + x) : make_uint4(0, 0, 0, 0);
-      nraw[4 * x] = y.x;
-      nraw[4 * x + 1] = y.y;
-      nraw[4 * x + 2] = y.z;
-      nraw[4 * x + 3] = y.w;
+      const uint4 y = __ldg(s + x);
+      raw[4 * x] = y.x;
+      raw[4 * x + 1] = y.y;
+      raw[4 * x + 2] = y.z;
+      raw[4 * x + 3] = y.w;
     }
   };
   auto open_row = [&](int row, int page) {   // parameters, and where the codes are
     nskip = row >= 0 && (page < 0 || page >= a.n_pool_pages);
     if (nskip) report(a.status, KVQ_DEV_BAD_PAGE);
-    const bool there = row >= 0 && !nskip;
+    const bool there = nthere = row >= 0 && !nskip;
+    // without a row, some row: its codes meet a scale of 0
+    const int slot = there ? row % P : 0;
     const uint8_t* sub = pool + (int64_t)(there ? page : 0) * page_bytes;
-    src = there ? sub + (row % P) * L.code_bytes : nullptr;
+    src = sub + slot * L.code_bytes;
     if constexpr (!F16) {
-      const uint8_t* par = sub + P * L.code_bytes + (there ? row % P : 0) * L.param_row_bytes;
+      const uint8_t* par = sub + P * L.code_bytes + slot * L.param_row_bytes;
 #pragma unroll
       for (int u = 0; u < NU; ++u) {
         nsc[u] = u ? nsc[u - (u > 0)] : 0.f;
@@ -290,7 +294,7 @@ __device__ void produce(const PrefillArgs& a, const PrefillTile& t, const KeyRan
       }
       return now;
     };
-    bool gone = src == nullptr;
+    bool gone = !nthere;
     if constexpr (!F16) {
       // the largest scale and bias of the step's keys
       float ms = 0.f, mb = 0.f;
@@ -313,15 +317,6 @@ __device__ void produce(const PrefillArgs& a, const PrefillTile& t, const KeyRan
     Scale s = {};
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
-      uint32_t raw[W];
-#pragma unroll
-      for (int x = 0; x < W; ++x) raw[x] = nraw[x];
-      if (p == NP - 1) {
-        open_row(row1, page1);
-        load_piece(0);
-      } else {
-        load_piece(p + 1);
-      }
 #pragma unroll
       for (int x = 0; x < CP; ++x) {
         const int d = 8 * (p * CP + x), h = d / 64, k = d % 64 / 8;   // eight dims from d: chunk k of block h
@@ -336,14 +331,14 @@ __device__ void produce(const PrefillArgs& a, const PrefillTile& t, const KeyRan
 #pragma unroll
             for (int v = 0; v < W; ++v) inf |= ((raw[v] & 0x7FFF7FFFu) + 0x04000400u) & 0x80008000u;
             zero = inf != 0;
-            bad |= zero;
+            bad |= zero && !gone;
           }
-          y = zero ? make_uint4(0, 0, 0, 0) : make_uint4(w[0], w[1], w[2], w[3]);
+          y = zero || gone ? make_uint4(0, 0, 0, 0) : make_uint4(w[0], w[1], w[2], w[3]);
         } else {
           if (d % 32 == 0) s = make_scale<KIND>(sc[F16 ? 0 : d / 32], bi[AFF ? d / 32 : 0]);
           y = dequant8<KIND>(w[0], w[CW - 1], s);
         }
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(ring + st * kBlockBytes + ((k ^ (pt & 7)) << 4)),
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"((ring + st * kBlockBytes) ^ (k << 4)),
                      "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w)
                      : "memory");
         if (k == 7) {
@@ -354,6 +349,13 @@ __device__ void produce(const PrefillArgs& a, const PrefillTile& t, const KeyRan
             if (lane == 0) mbar_arrive(smem_u32(&full[us][kh]));
           }
         }
+      }
+      // the next piece is on its way while this warp waits for room for it
+      if (p == NP - 1) {
+        open_row(row1, page1);
+        load_piece(0);
+      } else {
+        load_piece(p + 1);
       }
     }
     row1 = row2;
@@ -375,12 +377,12 @@ __device__ __forceinline__ void produce_kind(int kind, const PrefillArgs& a, con
 }
 
 // The queries of the na row tiles, rotated, scaled into fp16 and stored as
-// blocks of 64 dims; HD / 8 lanes share a row, and every warp of the CTA takes
-// part.
+// blocks of 64 dims; HD / 8 lanes share a row.  Every warp but the producers'
+// takes part, `warp` counted among those.
 template <int HD>
 __device__ void load_queries(const PrefillArgs& a, const PrefillTile& t, int rows, int na, int lg, int kvh, int warp,
                              int lane, Shared<HD>& sh) {
-  constexpr int HB = HD / 64, LANES = HD / 8, RPW = 32 / LANES, STEP = tc_threads(HD) / 32 * RPW;
+  constexpr int HB = HD / 64, LANES = HD / 8, RPW = 32 / LANES, STEP = (4 * row_tiles(HD) + 4) * RPW;
   const int li = lane % LANES;
   const bool neox = a.rope == KVQ_ROPE_NEOX;
   const int order = order_of(a.kl.kind);
@@ -453,12 +455,9 @@ __device__ void load_queries(const PrefillArgs& a, const PrefillTile& t, int row
     const int e = hold_exponent(top);
     const float down = pow2i(-e);
     if (li == 0) sh.qscale[R] = a.score_scale * pow2i(e);
-    __half y[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = __float2half_rn(x[i] * down);
-    auto word = [&](int i, int j) {
-      return (uint32_t)__half_as_ushort(y[i]) | (uint32_t)__half_as_ushort(y[j]) << 16;
-    };
+    for (int i = 0; i < 8; ++i) x[i] *= down;
+    auto word = [&](int i, int j) { return h2u(__floats2half2_rn(x[i], x[j])); };
     auto chunk = [&](int d) {   // address of the 16-byte chunk of dim d
       return base + (d / 64) * kBlockBytes + r * 128 + (((d % 64 / 8) ^ (r & 7)) << 4);
     };
@@ -475,10 +474,16 @@ __device__ void load_queries(const PrefillArgs& a, const PrefillTile& t, int row
                    "r"(w[3])
                    : "memory");
     } else {
+      // two runs of four dims: each half a chunk, or every other half of one
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < 8; i += 2) {
+        const uint32_t w = word(i, i + 1);
         const int d = (i < 4 ? d0 : d1) + i % 4;
-        asm volatile("st.shared.b16 [%0], %1;" ::"r"(chunk(d) + 2 * pos_of(order, d & 7)), "h"(__half_as_ushort(y[i]))
+        const uint32_t at = chunk(d);
+        asm volatile("st.shared.b16 [%0], %1;" ::"r"(at + 2 * pos_of(order, d & 7)), "h"((unsigned short)(w & 0xFFFFu))
+                     : "memory");
+        asm volatile("st.shared.b16 [%0], %1;" ::"r"(at + 2 * pos_of(order, (d + 1) & 7)),
+                     "h"((unsigned short)(w >> 16))
                      : "memory");
       }
     }
@@ -572,6 +577,7 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(smem_u32(&sh.ready[i]), 2);   // K's and V's
     }
+    mbar_init(smem_u32(&sh.qfull), 4 * MT + 4);
     for (int i = 0; i < MT; ++i) {
       for (int h = 0; h < 2; ++h) {
         mbar_init(smem_u32(&sh.sfull[i][h]), 1);
@@ -583,13 +589,18 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
     sh.stop = 0;
     mbar_init_fence();
   }
-  load_queries<HD>(a, t, rows, na, lg, kvh, warp, lane, sh);
-  fence_async_smem();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
   const uint32_t s_col = HD == 256 ? 256 : 0, o_col = HD == 256 ? 0 : 256;
 
+  if (warp < 4 * MT || warp >= kMmaWarp) {
+    load_queries<HD>(a, t, rows, na, lg, kvh, warp < 4 * MT ? warp : warp - 8, lane, sh);
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sh.qfull));
+    mbar_wait(smem_u32(&sh.qfull), 0, stop);
+  }
   if (warp < 4 * MT) {
     // ------------------------------------------------------------ softmax
     regs_set<regs_softmax(HD), regs_launch(HD)>();
@@ -706,6 +717,7 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
       const int64_t orow = out_row(mine ? R : 0);
       const float up = pow2i(held) * (a.n_splits > 1 ? 1.f : (l == 0.f ? 0.f : 1.f / l));
       const int order = order_of(a.vl.kind);
+      const uint32_t q_at = smem_u32(sh.q) + rt * HB * kBlockBytes;
       if (mine && a.n_splits > 1) a.ws_ml[ws0 + orow] = make_float2(m == -INFINITY ? m : m - kShift, l);
 #pragma unroll 1
       for (int d = 0; d < HD; d += 32) {
@@ -727,27 +739,46 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
 #pragma unroll
           for (int e = 0; e < 32; ++e) y[e] = o[e];
         }
-        if (!mine) continue;
-        if (a.n_splits == 1) {
-          uint32_t w[16];
+        if (a.n_splits == 1) {   // to the row's place of the query tile, no longer needed
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float y0 = y[2 * e] * up, y1 = y[2 * e + 1] * up;
-            if (a.act == KVQ_F16) {
-              w[e] = h2u(__floats2half2_rn(y0, y1));
-            } else {
-              const __nv_bfloat162 h = __floats2bfloat162_rn(y0, y1);
-              w[e] = *reinterpret_cast<const uint32_t*>(&h);
+          for (int c = 0; c < 4; ++c) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float y0 = y[8 * c + 2 * e] * up, y1 = y[8 * c + 2 * e + 1] * up;
+              if (a.act == KVQ_F16) {
+                w[e] = h2u(__floats2half2_rn(y0, y1));
+              } else {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(y0, y1);
+                w[e] = *reinterpret_cast<const uint32_t*>(&h);
+              }
             }
+            const int k = (d / 8 + c) & 7;
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                             q_at + (d / 64) * kBlockBytes + (R & 127) * 128 + ((k ^ (R & 7)) << 4)),
+                         "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                         : "memory");
           }
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<unsigned short*>(a.out) + orow * HD + d);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) dst[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
-        } else {
+        } else if (mine) {
           float4* dst = reinterpret_cast<float4*>(a.ws_acc + (ws0 + orow) * HD + d);
 #pragma unroll
           for (int e = 0; e < 8; ++e)
             dst[e] = make_float4(y[4 * e] * up, y[4 * e + 1] * up, y[4 * e + 2] * up, y[4 * e + 3] * up);
+        }
+      }
+      if (a.n_splits == 1) {   // whole rows at a time: HD / 8 lanes write one
+        constexpr int LANES = HD / 8, RPW = 32 / LANES;
+        __syncwarp();
+        const int c = lane % LANES;
+#pragma unroll 4
+        for (int k = 0; k < 32 / RPW; ++k) {
+          const int r = (warp & 3) * 32 + k * RPW + lane / LANES, Rr = rt * 128 + r;
+          uint4 y;
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(y.x), "=r"(y.y), "=r"(y.z), "=r"(y.w)
+                       : "r"(q_at + (c / 8) * kBlockBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4)));
+          if (Rr < rows)
+            *reinterpret_cast<uint4*>(static_cast<unsigned short*>(a.out) + out_row(Rr) * HD + 8 * c) = y;
         }
       }
       tc_fence_before();
