@@ -188,8 +188,8 @@ __device__ __forceinline__ uint4 dequant8(uint32_t w0, uint32_t w1, const Scale&
 // The dequantizing warpgroup of K or V: thread pt owns key pt of every step.
 // Loads run ahead of their use: a step's page id two steps, its parameters one
 // step, and its codes one piece (16 words of a row).
-template <int KIND, int HD, bool IS_V>
-__device__ void produce(const PrefillArgs& a, const PrefillTile& t, const KeyRange& kr, int j0, int n, int kvh, int pt,
+template <int KIND, int HD>
+__device__ void produce(const bool is_v, const PrefillArgs& a, const PrefillTile& t, const KeyRange& kr, int j0, int n, int kvh, int pt,
                         Shared<HD>& sh, volatile int* stop) {
   constexpr int P = 16, HB = HD / 64, UB = unit_blocks(HD);
   constexpr bool F16 = KIND == KVQ_F16_KV, AFF = KIND == KVQ_AFFINE_INT4;
@@ -198,14 +198,14 @@ __device__ void produce(const PrefillArgs& a, const PrefillTile& t, const KeyRan
   constexpr int NP = CW * HD / 8 / W;                              // pieces a row
   constexpr int CP = W / CW;                                       // eights a piece
   constexpr int NU = F16 ? 1 : HD / 32;                            // 32-dim units: groups are 32 dims or more
-  const PoolLayout& L = IS_V ? a.vl : a.kl;
-  const uint8_t* pool = (IS_V ? a.v_pool : a.k_pool) + (int64_t)kvh * L.sub_bytes;
+  const PoolLayout& L = is_v ? a.vl : a.kl;
+  const uint8_t* pool = (is_v ? a.v_pool : a.k_pool) + (int64_t)kvh * L.sub_bytes;
   const int32_t* bt = a.block_table + (int64_t)t.b * a.max_pages;
   const int warp = pt >> 5, lane = pt & 31;
   // its row of a block, and there the chunk that chunk 0 is stored at
-  const uint32_t ring = smem_u32(IS_V ? sh.v : sh.k) + pt * 128 + ((pt & 7) << 4);
-  uint64_t(*full)[2] = IS_V ? sh.vfull : sh.kfull;
-  uint64_t(*empty)[2] = IS_V ? sh.vempty : sh.kempty;
+  const uint32_t ring = smem_u32(is_v ? sh.v : sh.k) + pt * 128 + ((pt & 7) << 4);
+  uint64_t(*full)[2] = is_v ? sh.vfull : sh.kfull;
+  uint64_t(*empty)[2] = is_v ? sh.vempty : sh.kempty;
   const int kh = pt / kHalf;   // its half of the step
   const int pb = param_bytes(L.param);
   const int gmask = F16 ? 0 : L.group / 32 - 1;   // units a group (a power of two), less one
@@ -278,18 +278,18 @@ __device__ void produce(const PrefillArgs& a, const PrefillTile& t, const KeyRan
     auto publish = [&](int e) -> int {
       const uint32_t ws = __ballot_sync(0xffffffffu, skip), wb = __ballot_sync(0xffffffffu, bad);
       const int top = __reduce_max_sync(0xffffffffu, e);
-      int2* r = sh.red[IS_V][i & 1];
+      int2* r = sh.red[is_v][i & 1];
       if (lane == 0) {
         r[warp] = make_int2(top, ws | wb ? 1 : 0);
-        meta.skip[IS_V][warp] = ws;
-        meta.bad[IS_V][warp] = wb;
+        meta.skip[is_v][warp] = ws;
+        meta.bad[is_v][warp] = wb;
       }
-      group_sync(IS_V ? 2 : 1);
+      group_sync(is_v ? 2 : 1);
       const int2 r0 = r[0], r1 = r[1], r2 = r[2], r3 = r[3];
       const int all = max(max(r0.x, r1.x), max(r2.x, r3.x));
-      const int now = IS_V ? max(held, all) : all;
+      const int now = is_v ? max(held, all) : all;
       if (pt == 0) {
-        meta.head[IS_V] = make_int2(now, r0.y | r1.y | r2.y | r3.y);
+        meta.head[is_v] = make_int2(now, r0.y | r1.y | r2.y | r3.y);
         mbar_arrive(smem_u32(&sh.ready[i % kSlots]));
       }
       return now;
@@ -363,130 +363,129 @@ __device__ void produce(const PrefillArgs& a, const PrefillTile& t, const KeyRan
   }
 }
 
-template <int HD, bool IS_V>
-__device__ __forceinline__ void produce_kind(int kind, const PrefillArgs& a, const PrefillTile& t, const KeyRange& kr,
-                                             int j0, int n, int kvh, int pt, Shared<HD>& sh, volatile int* stop) {
+template <int HD>
+__device__ __forceinline__ void produce_kind(int kind, bool is_v, const PrefillArgs& a, const PrefillTile& t,
+                                             const KeyRange& kr, int j0, int n, int kvh, int pt, Shared<HD>& sh,
+                                             volatile int* stop) {
   switch (kind) {
-    case KVQ_SYM_INT4: return produce<KVQ_SYM_INT4, HD, IS_V>(a, t, kr, j0, n, kvh, pt, sh, stop);
-    case KVQ_SYM_INT8: return produce<KVQ_SYM_INT8, HD, IS_V>(a, t, kr, j0, n, kvh, pt, sh, stop);
-    case KVQ_AFFINE_INT4: return produce<KVQ_AFFINE_INT4, HD, IS_V>(a, t, kr, j0, n, kvh, pt, sh, stop);
-    case KVQ_SHIMMY_INT4: return produce<KVQ_SHIMMY_INT4, HD, IS_V>(a, t, kr, j0, n, kvh, pt, sh, stop);
+    case KVQ_SYM_INT4: return produce<KVQ_SYM_INT4, HD>(is_v, a, t, kr, j0, n, kvh, pt, sh, stop);
+    case KVQ_SYM_INT8: return produce<KVQ_SYM_INT8, HD>(is_v, a, t, kr, j0, n, kvh, pt, sh, stop);
+    case KVQ_AFFINE_INT4: return produce<KVQ_AFFINE_INT4, HD>(is_v, a, t, kr, j0, n, kvh, pt, sh, stop);
+    case KVQ_SHIMMY_INT4: return produce<KVQ_SHIMMY_INT4, HD>(is_v, a, t, kr, j0, n, kvh, pt, sh, stop);
     default:
-      if constexpr (HD <= 128) return produce<KVQ_F16_KV, HD, IS_V>(a, t, kr, j0, n, kvh, pt, sh, stop);
+      if constexpr (HD <= 128) return produce<KVQ_F16_KV, HD>(is_v, a, t, kr, j0, n, kvh, pt, sh, stop);
   }
 }
 
 // The queries of the na row tiles, rotated, scaled into fp16 and stored as
-// blocks of 64 dims; HD / 8 lanes share a row.  Every warp but the producers'
-// takes part, `warp` counted among those.
+// blocks of 64 dims.  HD / 8 lanes take the heads of a token, one after the
+// other.  The rows are first copied as they are, all at once, and then worked
+// on in place in a short loop: this code runs once a CTA, and what it costs is
+// its latency and its instructions' way into the caches.  Every warp but the
+// producers' takes part, `warp` counted among those.
 template <int HD>
 __device__ void load_queries(const PrefillArgs& a, const PrefillTile& t, int rows, int na, int lg, int kvh, int warp,
                              int lane, Shared<HD>& sh) {
   constexpr int HB = HD / 64, LANES = HD / 8, RPW = 32 / LANES, STEP = (4 * row_tiles(HD) + 4) * RPW;
-  const int li = lane % LANES;
-  const bool neox = a.rope == KVQ_ROPE_NEOX;
+  const int li = lane % LANES, first = warp * RPW + lane / LANES;
+  const bool neox = a.rope == KVQ_ROPE_NEOX, rope = a.rope != KVQ_ROPE_NONE, f16 = a.act == KVQ_F16;
   const int order = order_of(a.kl.kind);
   const int d0 = neox ? 4 * li : 8 * li, d1 = neox ? HD / 2 + 4 * li : 8 * li + 4;   // two runs of four
-  constexpr int BATCH = 4;   // rows whose loads are in flight together
+  const int tokens = na * 128 >> lg;   // the same number of rounds for every lane of a warp
+  const uint32_t base = smem_u32(sh.q);
+  auto row_at = [&](int R) { return base + (R >> 7) * HB * kBlockBytes + (R & 127) * 128; };
+  auto chunk = [&](int R, int d) { return row_at(R) + (d / 64) * kBlockBytes + (((d % 64 / 8) ^ (R & 7)) << 4); };
+  const unsigned short* q = static_cast<const unsigned short*>(a.q) + ((int64_t)t.row0 * a.n_heads + (kvh << lg)) * HD;
 #pragma unroll 1
-  for (int r0 = warp * RPW + lane / LANES; r0 < na * 128; r0 += BATCH * STEP) {
-    uint32_t qu[BATCH][4];
-    float4 cs[BATCH][2];
-#pragma unroll
-    for (int j = 0; j < BATCH; ++j) {
-      const int R = r0 + j * STEP;
-      qu[j][0] = qu[j][1] = qu[j][2] = qu[j][3] = 0;
-      cs[j][0] = cs[j][1] = make_float4(1.f, 0.f, 1.f, 0.f);
-      if (R < rows) {
-        const int64_t at = ((int64_t)(t.row0 + (R >> lg)) * a.n_heads + (kvh << lg) + (R & ((1 << lg) - 1))) * HD;
-        const unsigned short* q = static_cast<const unsigned short*>(a.q) + at;
-        const uint2 u0 = *reinterpret_cast<const uint2*>(q + d0), u1 = *reinterpret_cast<const uint2*>(q + d1);
-        qu[j][0] = u0.x;
-        qu[j][1] = u0.y;
-        qu[j][2] = u1.x;
-        qu[j][3] = u1.y;
-        if (a.rope != KVQ_ROPE_NONE) {   // both pairings meet pairs 4 li .. 4 li + 3
-          const float4* c =
-              reinterpret_cast<const float4*>(a.rope_tab + ((int64_t)(t.p0 + (R >> lg)) * (HD / 2) + 4 * li) * 2);
-          cs[j][0] = c[0];
-          cs[j][1] = c[1];
-        }
-      }
+  for (int k = first; k < tokens; k += STEP)
+#pragma unroll 1
+    for (int h = 0; h < 1 << lg; ++h) {
+      const int R = (k << lg) + h;
+      const bool there = R < rows;   // a row past the tile is zero
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(chunk(R, 8 * li)),
+                   "l"(q + (there ? ((int64_t)k * a.n_heads + h) * HD : 0) + 8 * li), "r"(there ? 16 : 0)
+                   : "memory");
     }
-#pragma unroll
-    for (int j = 0; j < BATCH; ++j) {
-    const int R = r0 + j * STEP, r = R & 127;
-    if (r0 - lane / LANES + j * STEP >= na * 128) break;   // the same for the whole warp
-    const uint32_t base = smem_u32(sh.q) + (R >> 7) * HB * kBlockBytes;
-    float x[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t u = qu[j][i];
-      if (a.act == KVQ_F16) {
-        const float2 f = __half22float2(u2h(u));
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
-      } else {
-        x[2 * i] = __uint_as_float(u << 16);
-        x[2 * i + 1] = __uint_as_float(u & 0xFFFF0000u);
-      }
+  auto rotation = [&](int k, float4 (&c)[2]) {   // both pairings meet pairs 4 li .. 4 li + 3
+    c[0] = c[1] = make_float4(1.f, 0.f, 1.f, 0.f);
+    if (rope && k << lg < rows) {
+      const float4* p = reinterpret_cast<const float4*>(a.rope_tab + ((int64_t)(t.p0 + k) * (HD / 2) + 4 * li) * 2);
+      c[0] = p[0];
+      c[1] = p[1];
     }
-    if (a.rope != KVQ_ROPE_NONE) {
-      const float c[4] = {cs[j][0].x, cs[j][0].z, cs[j][1].x, cs[j][1].z};
-      const float s[4] = {cs[j][0].y, cs[j][0].w, cs[j][1].y, cs[j][1].w};
+  };
+  float4 nc[2];
+  rotation(first, nc);
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncwarp();
+#pragma unroll 1
+  for (int k = first; k < tokens; k += STEP) {
+    const float c[4] = {nc[0].x, nc[0].z, nc[1].x, nc[1].z}, s[4] = {nc[0].y, nc[0].w, nc[1].y, nc[1].w};
+    rotation(k + STEP, nc);
+#pragma unroll 1
+    for (int h = 0; h < 1 << lg; ++h) {
+      const int R = (k << lg) + h;
+      const uint32_t at0 = chunk(R, d0) + 2 * (d0 & 7), at1 = chunk(R, d1) + 2 * (d1 & 7);
+      uint32_t u[4];
+      asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(u[0]), "=r"(u[1]) : "r"(at0) : "memory");
+      asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(u[2]), "=r"(u[3]) : "r"(at1) : "memory");
+      float x[8];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float p = neox ? x[i] : x[2 * i], m = neox ? x[4 + i] : x[2 * i + 1];
-        const float y0 = p * c[i] - m * s[i], y1 = p * s[i] + m * c[i];
-        if (neox) {
-          x[i] = y0;
-          x[4 + i] = y1;
-        } else {
-          x[2 * i] = y0;
-          x[2 * i + 1] = y1;
+        const float2 y = __half22float2(u2h(u[i]));
+        x[2 * i] = f16 ? y.x : __uint_as_float(u[i] << 16);
+        x[2 * i + 1] = f16 ? y.y : __uint_as_float(u[i] & 0xFFFF0000u);
+      }
+      if (neox) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float p = x[i], m = x[4 + i];
+          x[i] = p * c[i] - m * s[i];
+          x[4 + i] = p * s[i] + m * c[i];
+        }
+      } else if (rope) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float p = x[2 * i], m = x[2 * i + 1];
+          x[2 * i] = p * c[i] - m * s[i];
+          x[2 * i + 1] = p * s[i] + m * c[i];
         }
       }
-    }
-    float top = 0.f;
+      float top = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));
+      for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));
 #pragma unroll
-    for (int o = LANES / 2; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const int e = hold_exponent(top);
-    const float down = pow2i(-e);
-    if (li == 0) sh.qscale[R] = a.score_scale * pow2i(e);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] *= down;
-    auto word = [&](int i, int j) { return h2u(__floats2half2_rn(x[i], x[j])); };
-    auto chunk = [&](int d) {   // address of the 16-byte chunk of dim d
-      return base + (d / 64) * kBlockBytes + r * 128 + (((d % 64 / 8) ^ (r & 7)) << 4);
-    };
-    if (!neox) {   // the lane's eight dims are one chunk
-      uint32_t w[4];
-      if (order == 2) {
-        w[0] = word(0, 4), w[1] = word(1, 5), w[2] = word(2, 6), w[3] = word(3, 7);
-      } else if (order == 1) {
-        w[0] = word(0, 2), w[1] = word(1, 3), w[2] = word(4, 6), w[3] = word(5, 7);
-      } else {
-        w[0] = word(0, 1), w[1] = word(2, 3), w[2] = word(4, 5), w[3] = word(6, 7);
-      }
-      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(chunk(d0)), "r"(w[0]), "r"(w[1]), "r"(w[2]),
-                   "r"(w[3])
-                   : "memory");
-    } else {
-      // two runs of four dims: each half a chunk, or every other half of one
-#pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-        const uint32_t w = word(i, i + 1);
-        const int d = (i < 4 ? d0 : d1) + i % 4;
-        const uint32_t at = chunk(d);
-        asm volatile("st.shared.b16 [%0], %1;" ::"r"(at + 2 * pos_of(order, d & 7)), "h"((unsigned short)(w & 0xFFFFu))
+      for (int o = LANES / 2; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const int e = hold_exponent(top);
+      const float down = pow2i(-e);
+      if (li == 0) sh.qscale[R] = a.score_scale * pow2i(e);
+      auto word = [&](int i, int k) { return h2u(__floats2half2_rn(x[i] * down, x[k] * down)); };
+      if (!neox) {   // the lane's eight dims are one chunk
+        uint32_t w[4];
+        if (order == 2) {
+          w[0] = word(0, 4), w[1] = word(1, 5), w[2] = word(2, 6), w[3] = word(3, 7);
+        } else if (order == 1) {
+          w[0] = word(0, 2), w[1] = word(1, 3), w[2] = word(4, 6), w[3] = word(5, 7);
+        } else {
+          w[0] = word(0, 1), w[1] = word(2, 3), w[2] = word(4, 5), w[3] = word(6, 7);
+        }
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at0), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
                      : "memory");
-        asm volatile("st.shared.b16 [%0], %1;" ::"r"(at + 2 * pos_of(order, (d + 1) & 7)),
-                     "h"((unsigned short)(w >> 16))
-                     : "memory");
+      } else {   // two runs of four dims: each half a chunk, or every other half of one
+        __syncwarp();   // the lane that shares the chunk has read it
+#pragma unroll
+        for (int i = 0; i < 8; i += 2) {
+          const uint32_t w = word(i, i + 1);
+          const int d = (i < 4 ? d0 : d1) + i % 4;
+          const uint32_t at = chunk(R, d);
+          asm volatile("st.shared.b16 [%0], %1;" ::"r"(at + 2 * pos_of(order, d & 7)),
+                       "h"((unsigned short)(w & 0xFFFFu))
+                       : "memory");
+          asm volatile("st.shared.b16 [%0], %1;" ::"r"(at + 2 * pos_of(order, (d + 1) & 7)),
+                       "h"((unsigned short)(w >> 16))
+                       : "memory");
+        }
       }
-    }
     }
   }
 }
@@ -652,17 +651,13 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
             tmem_st8(o_at + d, o);
           }
         };
-        if (ve != held) {   // the same for every row
-          if (u > 0) scale_o(pow2i(held - ve));
-          held = ve;
-        }
         // The row's 64 scores, all in registers; P then takes the place of S.
         float x[2][32];
 #pragma unroll
         for (int c = 0; c < 2; ++c) tmem_ld32(s_at + 32 * c, x[c]);
 #pragma unroll
         for (int c = 0; c < 2; ++c) tmem_ld_wait(x[c]);
-        if (!whole) {
+        if (__builtin_expect(!whole, 0)) {
           RowMask mask;
           mask.hi = min(end - tb, pos - tb + 1);
           mask.lo = a.window == 0 ? 0 : pos - a.window + 1 - tb;
@@ -680,11 +675,12 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
           for (int e = 0; e < 4; ++e) mc[e] = fmaxf(mc[e], fmaxf(x[k / 32][k % 32 + e], x[k / 32][k % 32 + 4 + e]));
         const float mx = fmaxf(fmaxf(mc[0], mc[1]), fmaxf(mc[2], mc[3])) * f;
         const bool raise = mx > m + kLazy;
-        if (__any_sync(0xffffffffu, raise)) {
+        if (__builtin_expect(__any_sync(0xffffffffu, raise || ve != held), 0)) {
           const float co = raise ? ex2(m - mx) : 1.f;   // 2^-inf = 0: no key so far
           if (raise) m = mx;
           l *= co;
-          if (u > 0) scale_o(co);
+          if (u > 0) scale_o(co * pow2i(held - ve));
+          held = ve;
         }
         const float sub = m == -INFINITY ? 0.f : m - kShift;
         const uint64_t f2 = pack2(f, f), sub2 = pack2(-sub, -sub);
@@ -783,12 +779,11 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
       }
       tc_fence_before();
     }
-  } else if (warp < 4 * MT + 4) {
-    regs_set<regs_produce(HD), regs_launch(HD)>();
-    produce_kind<HD, false>(a.kl.kind, a, t, kr, j0, n, kvh, tid - 128 * MT, sh, stop);
   } else if (warp < kMmaWarp) {
+    // ------------------------------------------------------------ K and V: one code, half the instructions to fetch
     regs_set<regs_produce(HD), regs_launch(HD)>();
-    produce_kind<HD, true>(a.vl.kind, a, t, kr, j0, n, kvh, tid - 128 * MT - 128, sh, stop);
+    const bool is_v = warp >= 4 * MT + 4;
+    produce_kind<HD>(is_v ? a.vl.kind : a.kl.kind, is_v, a, t, kr, j0, n, kvh, (tid - 128 * MT) & 127, sh, stop);
   } else {
     // ------------------------------------------------------------ products
     regs_set<kRegsProducts, regs_launch(HD)>();   // the whole warpgroup, one warp of which works
