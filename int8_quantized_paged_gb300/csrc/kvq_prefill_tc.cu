@@ -62,9 +62,6 @@ constexpr float kLazy = 8.0f;            // the running maximum rises past +2^8 
 constexpr float kShift = 7.0f;           // P is held times 2^7
 
 __host__ __device__ constexpr int row_tiles(int hd) { return hd == 256 ? 1 : 2; }
-// Blocks that change hands together, half their keys at a time: a whole step's,
-// or at head_dim 256, where the ring holds one step only, one.
-__host__ __device__ constexpr int unit_blocks(int hd) { return hd == 256 ? 1 : hd / 64; }
 __host__ __device__ constexpr int tc_threads(int hd) { return 128 * row_tiles(hd) + 256 + 128; }
 // Registers a thread: at launch (65536 over the threads, in eights), then by
 // role.  A role may only take what the others gave back, so the shares must
@@ -97,7 +94,7 @@ struct Shared {
   StepMeta meta[kSlots];
   float qscale[MT * 128];   // f without the keys' part
   int2 red[2][2][4];
-  // half a unit each
+  // half a step's keys each
   uint64_t kfull[kStages][2], kempty[kStages][2], vfull[kStages][2], vempty[kStages][2];
   uint64_t ready[kSlots];   // a step's metadata are there
   uint64_t qfull;                        // the queries are there
@@ -185,104 +182,123 @@ __device__ __forceinline__ uint4 dequant8(uint32_t w0, uint32_t w1, const Scale&
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-// The dequantizing warpgroup of K or V: thread pt owns key pt of every step.
-// Loads run ahead of their use: a step's page id two steps, its parameters one
-// step, and its codes one piece (16 words of a row).
+// The dequantizing warpgroup of K or V.  A warp owns 32 keys of every step, two
+// pages.  Its loads are whole: LPR lanes share a row, 16 bytes each, so a load
+// covers KPL rows that lie one behind the other, and NL loads the 32 keys (a
+// thread to a row had every 16-byte load of a warp touch 32 rows: four to
+// eight times the passes through the L1, which the tensor cores read their
+// operands through as well).  Loads run ahead of their use: a step's page ids
+// two steps, its parameters and first codes one step.
 template <int KIND, int HD>
-__device__ void produce(const bool is_v, const PrefillArgs& a, const PrefillTile& t, const KeyRange& kr, int j0, int n, int kvh, int pt,
-                        Shared<HD>& sh, volatile int* stop) {
-  constexpr int P = 16, HB = HD / 64, UB = unit_blocks(HD);
+__device__ void produce(const bool is_v, const PrefillArgs& a, const PrefillTile& t, const KeyRange& kr, int j0, int n,
+                        int kvh, int pt, Shared<HD>& sh, volatile int* stop) {
+  constexpr int P = 16, HB = HD / 64, RU = kStages / HB;   // blocks a step, steps a ring
   constexpr bool F16 = KIND == KVQ_F16_KV, AFF = KIND == KVQ_AFFINE_INT4;
-  constexpr int CW = F16 ? 4 : (KIND == KVQ_SYM_INT8 ? 2 : 1);     // words of eight codes
-  constexpr int W = CW * HD / 8 < 16 ? CW * HD / 8 : 16;           // words of a piece
-  constexpr int NP = CW * HD / 8 / W;                              // pieces a row
-  constexpr int CP = W / CW;                                       // eights a piece
-  constexpr int NU = F16 ? 1 : HD / 32;                            // 32-dim units: groups are 32 dims or more
+  constexpr int BITS = F16 ? 16 : (KIND == KVQ_SYM_INT8 ? 8 : 4);
+  constexpr int LPR = HD * BITS / 128, KPL = 32 / LPR, NL = LPR;
+  constexpr int CPP = 16 / BITS, WPC = BITS / 4;           // eights of dims in 16 bytes, words of an eight
+  constexpr int NLP = NL < 8 ? NL : 8, NP = NL / NLP;      // loads kept in registers, and how often a step
+  constexpr int NS = F16 ? 1 : NL;
   const PoolLayout& L = is_v ? a.vl : a.kl;
   const uint8_t* pool = (is_v ? a.v_pool : a.k_pool) + (int64_t)kvh * L.sub_bytes;
   const int32_t* bt = a.block_table + (int64_t)t.b * a.max_pages;
-  const int warp = pt >> 5, lane = pt & 31;
-  // its row of a block, and there the chunk that chunk 0 is stored at
-  const uint32_t ring = smem_u32(is_v ? sh.v : sh.k) + pt * 128 + ((pt & 7) << 4);
+  const int warp = pt >> 5, lane = pt & 31, kh = warp / 2;   // kh: its half of the step
+  const int kq = lane / LPR, lp = lane % LPR;
+  const int dim0 = lp * (CPP * 8), blk = dim0 / 64;
+  // Where the lane's first eight dims of its key of load 0 are stored.  Lanes
+  // of a row that meet the same chunk of different blocks store their eights in
+  // another order (eight x in place of x ^ fl), so that they hit different banks.
+  const int fl = BITS == 4 ? (HD == 128 ? 2 * blk : (HD == 256 ? blk : 0)) : (BITS == 8 ? blk & 1 : 0);
+  const uint32_t dst0 = smem_u32(is_v ? sh.v : sh.k) + blk * kBlockBytes + (32 * warp + kq) * 128 +
+                        (((dim0 % 64 / 8) ^ (kq & 7) ^ fl) << 4);
   uint64_t(*full)[2] = is_v ? sh.vfull : sh.kfull;
   uint64_t(*empty)[2] = is_v ? sh.vempty : sh.kempty;
-  const int kh = pt / kHalf;   // its half of the step
   const int pb = param_bytes(L.param);
-  const int gmask = F16 ? 0 : L.group / 32 - 1;   // units a group (a power of two), less one
+  const int par0 = F16 ? 0 : P * L.code_bytes + dim0 / L.group * (AFF ? 2 : 1) * pb;   // of slot 0
   const int page_bytes = (int)L.page_bytes;       // a page is far below 2 GB
 
-  // Row of key pt in step i (-1: none), and its page id (-1 too).
-  auto row_at = [&](int i) -> int {
-    if (i >= n) return -1;
-    const int key = kr.base<kKeys>(j0 + i) + pt;
-    return key < kr.end(j0 + i) ? row_of(key, a.ring_rows, a.pin_rows) : -1;
-  };
-  auto page_at = [&](int row) -> int { return row >= 0 ? bt[row / P] : -1; };
-  uint32_t raw[W];
-  float nsc[NU], nbi[AFF ? NU : 1];
-  const uint8_t* src = pool;        // codes of the row being loaded
-  bool nthere = false, nskip = false;   // whether there is one; whether its page is bad
-  auto load_piece = [&](int p) {
-    const uint4* s = reinterpret_cast<const uint4*>(src + p * (4 * W));
+  // The warp's two page ids in step i (-1: no token there).
+  auto pages_at = [&](int i, int (&pg)[2]) {
+    pg[0] = pg[1] = -1;
+    if (i >= n) return;
+    const int key = kr.base<kKeys>(j0 + i) + 32 * warp, end = kr.end(j0 + i);
 #pragma unroll
-    for (int x = 0; x < W / 4; ++x) {
-      const uint4 y = __ldg(s + x);
+    for (int h = 0; h < 2; ++h)
+      if (key + P * h < end) pg[h] = bt[row_of(key + P * h, a.ring_rows, a.pin_rows) / P];
+  };
+  uint32_t raw[NLP * 4];
+  float nsc[NS], nbi[AFF ? NS : 1];
+  const uint8_t *sub[2] = {pool, pool};   // the pages being loaded
+  int keys = 0;                           // tokens of the step behind the warp's first key
+  uint32_t nskip = 0;                     // keys of bad pages
+  auto there = [&](int j) { return j * KPL + kq < keys && !((nskip >> (j * KPL & 16)) & 1u); };
+  auto load_piece = [&](int p) {
+#pragma unroll
+    for (int x = 0; x < NLP; ++x) {
+      const int j = p * NLP + x;
+      const uint4 y = __ldg(reinterpret_cast<const uint4*>(sub[j * KPL / P] + (j * KPL % P + kq) * (LPR * 16)) + lp);
       raw[4 * x] = y.x;
       raw[4 * x + 1] = y.y;
       raw[4 * x + 2] = y.z;
       raw[4 * x + 3] = y.w;
     }
   };
-  auto open_row = [&](int row, int page) {   // parameters, and where the codes are
-    nskip = row >= 0 && (page < 0 || page >= a.n_pool_pages);
-    if (nskip) report(a.status, KVQ_DEV_BAD_PAGE);
-    const bool there = nthere = row >= 0 && !nskip;
-    // without a row, some row: its codes meet a scale of 0
-    const int slot = there ? row % P : 0;
-    const uint8_t* sub = pool + (int64_t)(there ? page : 0) * page_bytes;
-    src = sub + slot * L.code_bytes;
-    if constexpr (!F16) {
-      const uint8_t* par = sub + P * L.code_bytes + slot * L.param_row_bytes;
+  auto open_step = [&](int i, const int (&pg)[2]) {   // the pages, and the parameters of the lane's keys
+    keys = i < n ? kr.end(j0 + i) - kr.base<kKeys>(j0 + i) - 32 * warp : 0;
+    nskip = 0;
 #pragma unroll
-      for (int u = 0; u < NU; ++u) {
-        nsc[u] = u ? nsc[u - (u > 0)] : 0.f;
-        if constexpr (AFF) nbi[u] = u ? nbi[u - (u > 0)] : 0.f;
-        if (there && (u & gmask) == 0) {   // parameters follow one another, group by group
-          nsc[u] = load_param(par, L.param);
-          par += pb;
-          if constexpr (AFF) {
-            nbi[u] = load_param(par, L.param);
-            par += pb;
-          }
-        }
+    for (int h = 0; h < 2; ++h) {
+      const bool tokens = P * h < keys, ok = pg[h] >= 0 && pg[h] < a.n_pool_pages;
+      if (tokens && !ok) {
+        nskip |= 0xFFFFu << (P * h);
+        if (lane == 0) report(a.status, KVQ_DEV_BAD_PAGE);
+      }
+      sub[h] = pool + (int64_t)(ok ? pg[h] : 0) * page_bytes;   // some page: its codes meet a scale of 0
+    }
+    if constexpr (!F16) {
+#pragma unroll
+      for (int j = 0; j < NL; ++j) {
+        const uint8_t* par = sub[j * KPL / P] + par0 + (j * KPL % P + kq) * L.param_row_bytes;
+        nsc[j] = load_param(par, L.param);
+        if constexpr (AFF) nbi[j] = load_param(par + pb, L.param);
       }
     }
   };
+  // One bit a key of 32 from a vote a load.
+  auto key_bits = [&](int j, bool x) -> uint32_t {
+    const uint32_t v = __ballot_sync(0xffffffffu, x);
+    uint32_t r = 0;
+    if (v != 0) {
+#pragma unroll 1
+      for (int k = 0; k < KPL; ++k)
+        if ((v >> (k * LPR)) & ((1u << LPR) - 1u)) r |= 1u << (j * KPL + k);
+    }
+    return r;
+  };
 
   int held = F16 ? 0 : -100;   // V: the exponent held so far
-  int row = row_at(0);
-  open_row(row, page_at(row));
+  int pg[2], pg1[2];
+  pages_at(0, pg);
+  open_step(0, pg);
   load_piece(0);
-  int row1 = row_at(1);
-  int page1 = page_at(row1);
+  pages_at(1, pg1);
 #pragma unroll 1
   for (int i = 0; i < n; ++i) {
-    const int row2 = row_at(i + 2);
-    const int page2 = page_at(row2);
+    int pg2[2];
+    pages_at(i + 2, pg2);
     StepMeta& meta = sh.meta[i % kSlots];
-    const bool skip = nskip;
-    bool bad = false;
-    float sc[NU], bi[AFF ? NU : 1];
+    const uint32_t skip = nskip;
+    uint32_t bad = 0;
+    float sc[NS], bi[AFF ? NS : 1];
     // Joins the warps' exponents and marks and leaves them for the softmax;
     // returns the exponent the step is held at (V: the largest so far).
     auto publish = [&](int e) -> int {
-      const uint32_t ws = __ballot_sync(0xffffffffu, skip), wb = __ballot_sync(0xffffffffu, bad);
       const int top = __reduce_max_sync(0xffffffffu, e);
       int2* r = sh.red[is_v][i & 1];
       if (lane == 0) {
-        r[warp] = make_int2(top, ws | wb ? 1 : 0);
-        meta.skip[is_v][warp] = ws;
-        meta.bad[is_v][warp] = wb;
+        r[warp] = make_int2(top, skip | bad ? 1 : 0);
+        meta.skip[is_v][warp] = skip;
+        meta.bad[is_v][warp] = bad;
       }
       group_sync(is_v ? 2 : 1);
       const int2 r0 = r[0], r1 = r[1], r2 = r[2], r3 = r[3];
@@ -294,72 +310,91 @@ __device__ void produce(const bool is_v, const PrefillArgs& a, const PrefillTile
       }
       return now;
     };
-    bool gone = !nthere;
     if constexpr (!F16) {
-      // the largest scale and bias of the step's keys
-      float ms = 0.f, mb = 0.f;
+      int e = -100;
+      bool odd = false;   // parameters that are not finite, of a key or of what lies behind the keys
 #pragma unroll
-      for (int u = 0; u < NU; ++u) {
-        bad |= !(nsc[u] < kMostScale) || (AFF && !isfinite(nbi[AFF ? u : 0]));
-        ms = fmaxf(ms, nsc[u]);
-        if constexpr (AFF) mb = fmaxf(mb, fabsf(nbi[u]));
+      for (int j = 0; j < NL; ++j) {
+        const bool fine = nsc[j] < kMostScale && (!AFF || isfinite(nbi[AFF ? j : 0]));
+        odd |= !fine;
+        if (fine && there(j)) e = max(e, key_exponent(nsc[j], AFF ? fabsf(nbi[AFF ? j : 0]) : 0.f));
       }
-      gone |= bad;
-      held = publish(gone ? -100 : key_exponent(ms, mb));
+      if (__builtin_expect(__any_sync(0xffffffffu, odd), 0)) {
+#pragma unroll
+        for (int j = 0; j < NL; ++j) {
+          const bool fine = nsc[j] < kMostScale && (!AFF || isfinite(nbi[AFF ? j : 0]));
+          bad |= key_bits(j, !fine && there(j));
+          if (!fine) {
+            nsc[j] = 0.f;
+            if constexpr (AFF) nbi[j] = 0.f;
+          }
+        }
+      }
+      held = publish(e);
       const float down = pow2i(-held);
 #pragma unroll
-      for (int u = 0; u < NU; ++u) {
-        sc[u] = gone ? 0.f : nsc[u] * down;
-        if constexpr (AFF) bi[u] = gone ? 0.f : nbi[u] * down;
+      for (int j = 0; j < NL; ++j) {
+        sc[j] = there(j) ? nsc[j] * down : 0.f;
+        if constexpr (AFF) bi[j] = there(j) ? nbi[j] * down : 0.f;
       }
     }
-    bool zero = false;
-    Scale s = {};
+    const int us = i % RU;
+    mbar_wait(smem_u32(&empty[us][kh]), (i / RU + 1) & 1, stop);
+    const uint32_t dst = dst0 + us * (HB * kBlockBytes);
 #pragma unroll
     for (int p = 0; p < NP; ++p) {
 #pragma unroll
-      for (int x = 0; x < CP; ++x) {
-        const int d = 8 * (p * CP + x), h = d / 64, k = d % 64 / 8;   // eight dims from d: chunk k of block h
-        const int st = (i * HB + h) % kStages;
-        const int un = i * (HB / UB) + h / UB, us = un % (kStages / UB);
-        if (k == 0 && h % UB == 0) mbar_wait(smem_u32(&empty[us][kh]), (un / (kStages / UB) + 1) & 1, stop);
-        const uint32_t* w = raw + x * CW;
-        uint4 y;
+      for (int x = 0; x < NLP; ++x) {
+        const int j = p * NLP + x;
+        uint32_t* w = raw + 4 * x;
+        const uint32_t row = (dst + j * KPL * 128) ^ ((j * KPL & 7) << 4);
         if constexpr (F16) {
-          if (x == 0) {   // a half with all exponent bits set carries into its sign bit
-            uint32_t inf = 0;
+          // a half with all exponent bits set carries into its sign bit
+          uint32_t inf = 0;
 #pragma unroll
-            for (int v = 0; v < W; ++v) inf |= ((raw[v] & 0x7FFF7FFFu) + 0x04000400u) & 0x80008000u;
-            zero = inf != 0;
-            bad |= zero && !gone;
-          }
-          y = zero || gone ? make_uint4(0, 0, 0, 0) : make_uint4(w[0], w[1], w[2], w[3]);
+          for (int v = 0; v < 4; ++v) inf |= ((w[v] & 0x7FFF7FFFu) + 0x04000400u) & 0x80008000u;
+          if (__builtin_expect(__any_sync(0xffffffffu, inf != 0), 0)) bad |= key_bits(j, inf != 0 && there(j));
+          const bool z = inf != 0 || !there(j);
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row), "r"(z ? 0u : w[0]), "r"(z ? 0u : w[1]),
+                       "r"(z ? 0u : w[2]), "r"(z ? 0u : w[3])
+                       : "memory");
         } else {
-          if (d % 32 == 0) s = make_scale<KIND>(sc[F16 ? 0 : d / 32], bi[AFF ? d / 32 : 0]);
-          y = dequant8<KIND>(w[0], w[CW - 1], s);
-        }
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"((ring + st * kBlockBytes) ^ (k << 4)),
-                     "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w)
-                     : "memory");
-        if (k == 7) {
-          if (F16 && h == HB - 1) publish(0);   // known only now
-          if ((h + 1) % UB == 0) {
-            fence_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&full[us][kh]));
+          const Scale s = make_scale<KIND>(sc[j], bi[AFF ? j : 0]);
+          auto swap = [&](int m, bool on) {   // eights x and x ^ m
+#pragma unroll
+            for (int v = 0; v < 4; ++v)
+              if (!(v & m)) {
+                const uint32_t lo = on ? w[v ^ m] : w[v], hi = on ? w[v] : w[v ^ m];
+                w[v] = lo;
+                w[v ^ m] = hi;
+              }
+          };
+          if constexpr (BITS == 4 && HD == 128) swap(2, fl & 2);
+          if constexpr (BITS == 4 && HD == 256) {
+            swap(1, fl & 1);
+            swap(2, fl & 2);
+          }
+          if constexpr (BITS == 8 && HD > 64) swap(2, fl & 1);   // an eight is two words
+#pragma unroll
+          for (int c = 0; c < CPP; ++c) {
+            const uint4 y = dequant8<KIND>(w[c * WPC], w[c * WPC + WPC - 1], s);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row ^ (c << 4)), "r"(y.x), "r"(y.y),
+                         "r"(y.z), "r"(y.w)
+                         : "memory");
           }
         }
       }
-      // the next piece is on its way while this warp waits for room for it
-      if (p == NP - 1) {
-        open_row(row1, page1);
-        load_piece(0);
-      } else {
-        load_piece(p + 1);
-      }
+      if (p < NP - 1) load_piece(p + 1);
     }
-    row1 = row2;
-    page1 = page2;
+    if (F16) publish(0);   // known only now
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&full[us][kh]));
+    // the next step is on its way while this warp waits for room for it
+    open_step(i + 1, pg1);
+    load_piece(0);
+    pg1[0] = pg2[0];
+    pg1[1] = pg2[1];
   }
 }
 
@@ -794,8 +829,8 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
       // the operands then stay in uniform registers, where the instruction
       // takes them (a lone lane in a branch of its own spent 120 cycles on each
       // product, twice its length).
-      constexpr int UB = unit_blocks(HD), NUN = HB / UB, RU = kStages / UB;   // units a step, units a ring
-      constexpr uint32_t id_qk = idesc_f16(kHalf, false), id_pv = idesc_f16(64 * UB, true);
+      constexpr int RU = kStages / HB;   // steps a ring
+      constexpr uint32_t id_qk = idesc_f16(kHalf, false), id_pv = idesc_f16(HD, true);
       constexpr int kHalfBytes = kHalf * 128;   // half the keys of a block
       // descriptors count addresses in 16 bytes
       const uint64_t qd = smem_desc(smem_u32(sh.q) + rt * HB * kBlockBytes, 16), kd = smem_desc(smem_u32(sh.k), 16),
@@ -805,42 +840,34 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
       const uint32_t s_at = __shfl_sync(0xffffffffu, tmem, 0) + s_col + rt * 128;
       const uint32_t o_at = __shfl_sync(0xffffffffu, tmem, 0) + o_col + rt * HD;
       auto qk = [&](int u) {   // scores of half step u
-        const int i = u >> 1, hf = u & 1;
+        const int i = u >> 1, hf = u & 1, us = i % RU;
+        mbar_wait(smem_u32(&sh.kfull[us][hf]), (i / RU) & 1, stop);
+        tc_fence_after();
+        if (leader) {
+          const uint64_t b = kd + (us * HB * kBlockBytes + hf * kHalfBytes) / 16;
 #pragma unroll
-        for (int g = 0; g < NUN; ++g) {
-          const int un = i * NUN + g, us = un % RU;
-          mbar_wait(smem_u32(&sh.kfull[us][hf]), (un / RU) & 1, stop);
-          tc_fence_after();
-          if (leader) {
-            const uint64_t b = kd + (us * UB * kBlockBytes + hf * kHalfBytes) / 16;
-#pragma unroll
-            for (int k = 0; k < 4 * UB; ++k)
-              mma_ss(s_at + hf * 64, qd + ((g * UB + k / 4) * kBlockBytes + 32 * (k % 4)) / 16,
-                     b + ((k / 4) * kBlockBytes + 32 * (k % 4)) / 16, id_qk, g > 0 || k > 0);
-            mma_commit(smem_u32(&sh.kempty[us][hf]));
-            if (g == NUN - 1) mma_commit(smem_u32(&sh.sfull[rt][hf]));
-          }
-          __syncwarp();
+          for (int k = 0; k < 4 * HB; ++k)
+            mma_ss(s_at + hf * 64, qd + ((k / 4) * kBlockBytes + 32 * (k % 4)) / 16,
+                   b + ((k / 4) * kBlockBytes + 32 * (k % 4)) / 16, id_qk, k > 0);
+          mma_commit(smem_u32(&sh.kempty[us][hf]));
+          mma_commit(smem_u32(&sh.sfull[rt][hf]));
         }
+        __syncwarp();
       };
       auto pv = [&](int u) {   // O of half step u
-        const int i = u >> 1, hf = u & 1;
+        const int i = u >> 1, hf = u & 1, us = i % RU;
+        mbar_wait(smem_u32(&sh.vfull[us][hf]), (i / RU) & 1, stop);
         mbar_wait(smem_u32(&sh.pfull[rt][hf]), i & 1, stop);
+        tc_fence_after();
+        if (leader) {
+          const uint64_t b = vd + (us * HB * kBlockBytes + hf * kHalfBytes) / 16;
 #pragma unroll
-        for (int g = 0; g < NUN; ++g) {
-          const int un = i * NUN + g, us = un % RU;
-          mbar_wait(smem_u32(&sh.vfull[us][hf]), (un / RU) & 1, stop);
-          tc_fence_after();
-          if (leader) {
-            const uint64_t b = vd + (us * UB * kBlockBytes + hf * kHalfBytes) / 16;
-#pragma unroll
-            for (int k = 0; k < kHalf / 16; ++k)
-              mma_ts(o_at + 64 * UB * g, s_at + hf * 64 + 8 * k, b + 2048 * k / 16, id_pv, u > 0 || k > 0);
-            mma_commit(smem_u32(&sh.vempty[us][hf]));
-            if (g == NUN - 1) mma_commit(smem_u32(&sh.ofull[rt][hf]));
-          }
-          __syncwarp();
+          for (int k = 0; k < kHalf / 16; ++k)
+            mma_ts(o_at, s_at + hf * 64 + 8 * k, b + 2048 * k / 16, id_pv, u > 0 || k > 0);
+          mma_commit(smem_u32(&sh.vempty[us][hf]));
+          mma_commit(smem_u32(&sh.ofull[rt][hf]));
         }
+        __syncwarp();
       };
       // Scores run two half steps ahead of the weights, in two buffers.
       if (nh > 0) qk(0);
@@ -853,18 +880,14 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
       // blocks behind this row tile's queries are given back unread
 #pragma unroll 1
       for (int u = nh; u < 2 * n; ++u) {
-        const int i = u >> 1, hf = u & 1;
-#pragma unroll
-        for (int g = 0; g < NUN; ++g) {
-          const int un = i * NUN + g, us = un % RU;
-          mbar_wait(smem_u32(&sh.kfull[us][hf]), (un / RU) & 1, stop);
-          mbar_wait(smem_u32(&sh.vfull[us][hf]), (un / RU) & 1, stop);
-          if (leader) {
-            mma_commit(smem_u32(&sh.kempty[us][hf]));
-            mma_commit(smem_u32(&sh.vempty[us][hf]));
-          }
-          __syncwarp();
+        const int i = u >> 1, hf = u & 1, us = i % RU;
+        mbar_wait(smem_u32(&sh.kfull[us][hf]), (i / RU) & 1, stop);
+        mbar_wait(smem_u32(&sh.vfull[us][hf]), (i / RU) & 1, stop);
+        if (leader) {
+          mma_commit(smem_u32(&sh.kempty[us][hf]));
+          mma_commit(smem_u32(&sh.vempty[us][hf]));
         }
+        __syncwarp();
       }
       if (leader) mma_commit(smem_u32(&sh.drain[rt]));
       __syncwarp();
