@@ -207,41 +207,82 @@ __global__ void __launch_bounds__(kSimtThreads) prefill_simt_kernel(const __grid
 }
 
 // ---------------------------------------------------------------- combine
-// One thread per four outputs of a tile; a split that saw no key has m = -inf
-// and its sums are not read.
-__global__ void __launch_bounds__(256) prefill_combine_kernel(const __grid_constant__ PrefillArgs a, int hd) {
+// One warp a row: its lanes hold the splits' weights, four outputs a lane (or
+// twice four) the sums, eight splits in flight.  A split that saw no key has
+// l = 0 and its sums are not read.
+constexpr int kMaxSplits = 160;
+template <int HD>
+__global__ void __launch_bounds__(256) prefill_combine_kernel(const __grid_constant__ PrefillArgs a) {
+  constexpr int NV = (HD + 127) / 128, NW = kMaxSplits / 32;   // float4s a lane, weights a lane
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int kvh = blockIdx.y, G = a.n_heads / a.n_kv_heads;
+  const int kvh = blockIdx.y, G = a.n_heads / a.n_kv_heads, lane = threadIdx.x & 31;
   PrefillTile t;
   if (!find_tile(a, blockIdx.x, false, &t) || t.zero) return;
-  const int n4 = t.cnt * G * (hd / 4);
   const int64_t stride = (int64_t)a.n_rows * a.n_heads;
-  for (int i = blockIdx.z * blockDim.x + threadIdx.x; i < n4; i += gridDim.z * blockDim.x) {
-    const int r = i / (hd / 4), d = i % (hd / 4) * 4;
+  for (int r = blockIdx.z * 8 + (threadIdx.x >> 5); r < t.cnt * G; r += gridDim.z * 8) {
     const int64_t o = (int64_t)(t.row0 + r / G) * a.n_heads + kvh * G + r % G;
+    float2 ml[NW];
     float M = -INFINITY;
-    for (int s = 0; s < a.n_splits; ++s) M = fmaxf(M, a.ws_ml[s * stride + o].x);
-    float l = 0.f;
-    float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s = 0; s < a.n_splits; ++s) {
-      const float2 ml = a.ws_ml[s * stride + o];
-      // a split with no attended key; one whose only keys were not finite has
-      // l NaN and keeps its weight
-      if (ml.y == 0.f) continue;
-      const float w = ml.x == -INFINITY ? 1.f : exp2f(ml.x - M);
-      const float4 x = *reinterpret_cast<const float4*>(a.ws_acc + (s * stride + o) * hd + d);
-      l = fmaf(w, ml.y, l);
-      y.x = fmaf(w, x.x, y.x);
-      y.y = fmaf(w, x.y, y.y);
-      y.z = fmaf(w, x.z, y.z);
-      y.w = fmaf(w, x.w, y.w);
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      const int s = lane + 32 * i;
+      ml[i] = s < a.n_splits ? a.ws_ml[s * stride + o] : make_float2(-INFINITY, 0.f);
+    }
+#pragma unroll
+    for (int i = 0; i < NW; ++i) M = fmaxf(M, ml[i].x);
+#pragma unroll
+    for (int x = 16; x >= 1; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+    float w[NW], l = 0.f;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+      // a split whose only keys were not finite has m = -inf and l NaN, and keeps its weight
+      w[i] = ml[i].y == 0.f ? 0.f : (ml[i].x == -INFINITY ? 1.f : exp2f(ml[i].x - M));
+      l += ml[i].y == 0.f ? 0.f : w[i] * ml[i].y;
+    }
+#pragma unroll
+    for (int x = 16; x >= 1; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+    float4 y[NV];
+#pragma unroll
+    for (int v = 0; v < NV; ++v) y[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+    const bool on = HD >= 128 || lane < HD / 4;
+    for (int s0 = 0; s0 < a.n_splits; s0 += 8) {
+      float ws[8];
+      float4 x[8][NV];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int s = s0 + k;
+        float pick = w[0];
+#pragma unroll
+        for (int i = 1; i < NW; ++i) pick = s0 / 32 == i ? w[i] : pick;
+        ws[k] = __shfl_sync(0xffffffffu, pick, s & 31);
+        if (s >= a.n_splits) ws[k] = 0.f;
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+          x[k][v] = on && !(ws[k] == 0.f)
+                        ? *reinterpret_cast<const float4*>(a.ws_acc + (s * stride + o) * HD + 4 * (lane + 32 * v))
+                        : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          y[v].x = fmaf(ws[k], x[k][v].x, y[v].x);
+          y[v].y = fmaf(ws[k], x[k][v].y, y[v].y);
+          y[v].z = fmaf(ws[k], x[k][v].z, y[v].z);
+          y[v].w = fmaf(ws[k], x[k][v].w, y[v].w);
+        }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    store_act(a.out, a.act, o * hd + d, y.x * inv);
-    store_act(a.out, a.act, o * hd + d + 1, y.y * inv);
-    store_act(a.out, a.act, o * hd + d + 2, y.z * inv);
-    store_act(a.out, a.act, o * hd + d + 3, y.w * inv);
+    if (on)
+#pragma unroll
+      for (int v = 0; v < NV; ++v) {
+        const int64_t at = o * HD + 4 * (lane + 32 * v);
+        store_act(a.out, a.act, at, y[v].x * inv);
+        store_act(a.out, a.act, at + 1, y[v].y * inv);
+        store_act(a.out, a.act, at + 2, y[v].z * inv);
+        store_act(a.out, a.act, at + 3, y[v].w * inv);
+      }
   }
 }
 
@@ -256,8 +297,8 @@ struct PrefillPlan {
 // Tiles and key splits.  A sequence's tiles are at most n_b / tq + 1, so
 // n_rows / tq + batch of them cover every case.  Keys are split while the
 // tiles leave SMs idle, into parts of at least kMinSplitKeys keys of the
-// longest range the table allows.
-constexpr int kMinSplitKeys = 256;
+// longest range the table allows: two steps of either kernel.
+constexpr int kMinSplitKeys = 256, kMinSplitKeysSimt = 2 * kSimtKeys;
 
 // Whether the tensor-core kernel takes this config: 16-bit activations (its
 // operands are fp16) and scale groups of whole 32-dim units.
@@ -284,8 +325,9 @@ static PrefillPlan make_prefill_plan(const kvq_config& c, int32_t batch, int32_t
   if (busy < batch) busy = batch < n_rows ? batch : n_rows;
   busy *= c.n_kv_heads;
   int64_t s = busy > 0 ? num_sms() / busy : 1;
-  const int64_t most = keys / kMinSplitKeys;
+  const int64_t most = keys / (p.tc ? kMinSplitKeys : kMinSplitKeysSimt);
   if (s > most) s = most;
+  if (s > kMaxSplits) s = kMaxSplits;
   p.n_splits = (int)(s < 1 ? 1 : s);
   const size_t units = p.n_splits > 1 ? (size_t)p.n_splits * n_rows * c.n_heads : 0;
   p.ml_offset = (units * c.head_dim * sizeof(float) + 255) / 256 * 256;
@@ -399,7 +441,11 @@ extern "C" kvq_status kvq_prefill_attention(const kvq_config* cfg, int32_t batch
     lc.gridDim = dim3((unsigned)p.n_tiles, (unsigned)cfg->n_kv_heads, 8);
     lc.blockDim = dim3(256);
     lc.dynamicSmemBytes = 0;
-    e = cudaLaunchKernelEx(&lc, prefill_combine_kernel, a, cfg->head_dim);
+    switch (cfg->head_dim) {
+      case 64: e = cudaLaunchKernelEx(&lc, prefill_combine_kernel<64>, a); break;
+      case 128: e = cudaLaunchKernelEx(&lc, prefill_combine_kernel<128>, a); break;
+      default: e = cudaLaunchKernelEx(&lc, prefill_combine_kernel<256>, a); break;
+    }
   }
   if (e == cudaSuccess) e = cudaGetLastError();
   if (e != cudaSuccess) return fail(KVQ_ERR_CUDA, "prefill launch: %s", cudaGetErrorString(e));

@@ -44,6 +44,8 @@
 // KVQ_DEV_TIMEOUT.
 #include <cuda_runtime.h>
 
+#include <atomic>
+
 #include "kvq_prefill.cuh"
 #include "kvq_prefill_tc.h"
 #include "kvq_umma_ptx.cuh"
@@ -412,21 +414,21 @@ __device__ __forceinline__ void produce_kind(int kind, bool is_v, const PrefillA
   }
 }
 
-// The queries of the na row tiles, rotated, scaled into fp16 and stored as
+// The queries of the CTA's rows, rotated, scaled into fp16 and stored as
 // blocks of 64 dims.  HD / 8 lanes take the heads of a token, one after the
 // other.  The rows are first copied as they are, all at once, and then worked
 // on in place in a short loop: this code runs once a CTA, and what it costs is
 // its latency and its instructions' way into the caches.  Every warp but the
 // producers' takes part, `warp` counted among those.
 template <int HD>
-__device__ void load_queries(const PrefillArgs& a, const PrefillTile& t, int rows, int na, int lg, int kvh, int warp,
+__device__ void load_queries(const PrefillArgs& a, const PrefillTile& t, int rows, int lg, int kvh, int warp,
                              int lane, Shared<HD>& sh) {
   constexpr int HB = HD / 64, LANES = HD / 8, RPW = 32 / LANES, STEP = (4 * row_tiles(HD) + 4) * RPW;
   const int li = lane % LANES, first = warp * RPW + lane / LANES;
   const bool neox = a.rope == KVQ_ROPE_NEOX, rope = a.rope != KVQ_ROPE_NONE, f16 = a.act == KVQ_F16;
   const int order = order_of(a.kl.kind);
   const int d0 = neox ? 4 * li : 8 * li, d1 = neox ? HD / 2 + 4 * li : 8 * li + 4;   // two runs of four
-  const int tokens = na * 128 >> lg;   // the same number of rounds for every lane of a warp
+  const int tokens = (rows + (1 << lg) - 1) >> lg;   // rows behind them stay as they are: no result comes from them
   const uint32_t base = smem_u32(sh.q);
   auto row_at = [&](int R) { return base + (R >> 7) * HB * kBlockBytes + (R & 127) * 128; };
   auto chunk = [&](int R, int d) { return row_at(R) + (d / 64) * kBlockBytes + (((d % 64 / 8) ^ (R & 7)) << 4); };
@@ -434,16 +436,13 @@ __device__ void load_queries(const PrefillArgs& a, const PrefillTile& t, int row
 #pragma unroll 1
   for (int k = first; k < tokens; k += STEP)
 #pragma unroll 1
-    for (int h = 0; h < 1 << lg; ++h) {
-      const int R = (k << lg) + h;
-      const bool there = R < rows;   // a row past the tile is zero
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(chunk(R, 8 * li)),
-                   "l"(q + (there ? ((int64_t)k * a.n_heads + h) * HD : 0) + 8 * li), "r"(there ? 16 : 0)
+    for (int h = 0; h < 1 << lg; ++h)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(chunk((k << lg) + h, 8 * li)),
+                   "l"(q + ((int64_t)k * a.n_heads + h) * HD + 8 * li)
                    : "memory");
-    }
   auto rotation = [&](int k, float4 (&c)[2]) {   // both pairings meet pairs 4 li .. 4 li + 3
     c[0] = c[1] = make_float4(1.f, 0.f, 1.f, 0.f);
-    if (rope && k << lg < rows) {
+    if (rope && k < tokens) {
       const float4* p = reinterpret_cast<const float4*>(a.rope_tab + ((int64_t)(t.p0 + k) * (HD / 2) + 4 * li) * 2);
       c[0] = p[0];
       c[1] = p[1];
@@ -454,12 +453,13 @@ __device__ void load_queries(const PrefillArgs& a, const PrefillTile& t, int row
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncwarp();
 #pragma unroll 1
-  for (int k = first; k < tokens; k += STEP) {
+  for (int k = first; k - lane / LANES < tokens; k += STEP) {   // the same count for every lane of a warp
+    const bool there = k < tokens;
     const float c[4] = {nc[0].x, nc[0].z, nc[1].x, nc[1].z}, s[4] = {nc[0].y, nc[0].w, nc[1].y, nc[1].w};
     rotation(k + STEP, nc);
 #pragma unroll 1
     for (int h = 0; h < 1 << lg; ++h) {
-      const int R = (k << lg) + h;
+      const int R = ((there ? k : 0) << lg) + h;
       const uint32_t at0 = chunk(R, d0) + 2 * (d0 & 7), at1 = chunk(R, d1) + 2 * (d1 & 7);
       uint32_t u[4];
       asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(u[0]), "=r"(u[1]) : "r"(at0) : "memory");
@@ -493,6 +493,8 @@ __device__ void load_queries(const PrefillArgs& a, const PrefillTile& t, int row
       for (int o = LANES / 2; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
       const int e = hold_exponent(top);
       const float down = pow2i(-e);
+      __syncwarp();   // the lane that shares a chunk has read it
+      if (!there) continue;
       if (li == 0) sh.qscale[R] = a.score_scale * pow2i(e);
       auto word = [&](int i, int k) { return h2u(__floats2half2_rn(x[i] * down, x[k] * down)); };
       if (!neox) {   // the lane's eight dims are one chunk
@@ -507,7 +509,6 @@ __device__ void load_queries(const PrefillArgs& a, const PrefillTile& t, int row
         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at0), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
                      : "memory");
       } else {   // two runs of four dims: each half a chunk, or every other half of one
-        __syncwarp();   // the lane that shares the chunk has read it
 #pragma unroll
         for (int i = 0; i < 8; i += 2) {
           const uint32_t w = word(i, i + 1);
@@ -629,7 +630,7 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
   const uint32_t s_col = HD == 256 ? 256 : 0, o_col = HD == 256 ? 0 : 256;
 
   if (warp < 4 * MT || warp >= kMmaWarp) {
-    load_queries<HD>(a, t, rows, na, lg, kvh, warp < 4 * MT ? warp : warp - 8, lane, sh);
+    load_queries<HD>(a, t, rows, lg, kvh, warp < 4 * MT ? warp : warp - 8, lane, sh);
     fence_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&sh.qfull));
@@ -643,7 +644,7 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
       const int R = rt * 128 + (tid & 127);
       const int pos = t.p0 + (min(R, rows - 1) >> lg);
       const int pmin = t.p0 + (rt * 128 >> lg), pmax = last_pos(rt);
-      const float qs = sh.qscale[R];
+      const float qs = R < rows ? sh.qscale[R] : 0.f;
       const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // this warp's 32 lanes of tensor memory
       const uint32_t o_at = tmem + lanes + o_col + rt * HD;
       const int nh = half_steps(rt);
@@ -907,14 +908,22 @@ template <int HD>
 cudaError_t launch(cudaLaunchConfig_t& lc, const PrefillArgs& a) {
   lc.blockDim = dim3(tc_threads(HD));
   lc.dynamicSmemBytes = shared_bytes<HD>();
-  // the roles' register split counts on the launch's share
-  cudaFuncAttributes at;
-  cudaError_t e = cudaFuncGetAttributes(&at, prefill_tc_kernel<HD>);
+  static std::atomic<bool> ready[64];   // by device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  if (at.numRegs < regs_launch(HD)) return cudaErrorLaunchOutOfResources;
-  e = cudaFuncSetAttribute(prefill_tc_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)shared_bytes<HD>());
-  return e != cudaSuccess ? e : cudaLaunchKernelEx(&lc, prefill_tc_kernel<HD>, a);
+  if (dev < 0 || dev >= 64 || !ready[dev].load(std::memory_order_acquire)) {
+    // the roles' register split counts on the launch's share
+    cudaFuncAttributes at;
+    e = cudaFuncGetAttributes(&at, prefill_tc_kernel<HD>);
+    if (e != cudaSuccess) return e;
+    if (at.numRegs < regs_launch(HD)) return cudaErrorLaunchOutOfResources;
+    e = cudaFuncSetAttribute(prefill_tc_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             (int)shared_bytes<HD>());
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64) ready[dev].store(true, std::memory_order_release);
+  }
+  return cudaLaunchKernelEx(&lc, prefill_tc_kernel<HD>, a);
 }
 
 }  // namespace

@@ -29,18 +29,36 @@ struct ReadArgs {
   void* v_out;
   int32_t* status;
   int64_t n_units;   // n_rows * n_kv_heads * head_dim / 16
+  int32_t wide;      // both outputs are 32-byte aligned
   int32_t n_kv_heads, n_seqs, max_pages, ring_rows, pin_rows, n_pool_pages;
   PoolLayout kl, vl;
 };
 
-template <int ACT>
-__device__ __forceinline__ void write16(void* out, int64_t i, const float (&x)[16]) {
-  if constexpr (ACT == KVQ_F32) {
-    float4* p = reinterpret_cast<float4*>(static_cast<float*>(out) + i);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) p[j] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+// 32 bytes in one store where p is 32-byte aligned (WIDE), which writes whole
+// sectors, else in two.
+template <bool WIDE>
+__device__ __forceinline__ void store32(void* p, const uint32_t (&w)[8]) {
+  if constexpr (WIDE) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
   } else {
-    uint32_t w[8];
+    static_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    static_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
+template <int ACT, bool WIDE>
+__device__ __forceinline__ void write16(void* out, int64_t i, const float (&x)[16]) {
+  uint32_t w[8];
+  if constexpr (ACT == KVQ_F32) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(x[8 * h + j]);
+      store32<WIDE>(static_cast<float*>(out) + i + 8 * h, w);
+    }
+  } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       if constexpr (ACT == KVQ_F16) {
@@ -51,14 +69,12 @@ __device__ __forceinline__ void write16(void* out, int64_t i, const float (&x)[1
         w[j] = *reinterpret_cast<const uint32_t*>(&h);
       }
     }
-    uint4* p = reinterpret_cast<uint4*>(static_cast<unsigned short*>(out) + i);
-    p[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    p[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    store32<WIDE>(static_cast<unsigned short*>(out) + i, w);
   }
 }
 
 template <int KK, int VK, int HD, int ACT>
-__global__ void __launch_bounds__(256) read_kernel(const ReadArgs a) {
+__global__ void __launch_bounds__(256, 8) read_kernel(const __grid_constant__ ReadArgs a) {
   constexpr int P = 16, U = HD / 16;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -87,11 +103,13 @@ __global__ void __launch_bounds__(256) read_kernel(const ReadArgs a) {
   float x[16];
   if (a.k_out) {
     read16<KK>(a.k_pool + page * a.kl.page_bytes + (int64_t)head * a.kl.sub_bytes, a.kl, r % P, u, x);
-    write16<ACT>(a.k_out, i * 16, x);
+    if (a.wide) write16<ACT, true>(a.k_out, i * 16, x);
+    else write16<ACT, false>(a.k_out, i * 16, x);
   }
   if (a.v_out) {
     read16<VK>(a.v_pool + page * a.vl.page_bytes + (int64_t)head * a.vl.sub_bytes, a.vl, r % P, u, x);
-    write16<ACT>(a.v_out, i * 16, x);
+    if (a.wide) write16<ACT, true>(a.v_out, i * 16, x);
+    else write16<ACT, false>(a.v_out, i * 16, x);
   }
 }
 
@@ -143,6 +161,7 @@ extern "C" kvq_status kvq_read(const kvq_config* cfg, int32_t n_rows, const int3
   a.n_units = (int64_t)n_rows * cfg->n_kv_heads * (cfg->head_dim / 16);
   a.n_kv_heads = cfg->n_kv_heads; a.n_seqs = n_seqs; a.max_pages = max_pages_per_seq;
   a.ring_rows = ring_rows; a.pin_rows = pinned_rows(*cfg, ring_rows, sinks); a.n_pool_pages = n_pool_pages;
+  a.wide = ((reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out)) & 31) == 0;
   a.kl = pool_layout(*cfg, 0);
   a.vl = pool_layout(*cfg, 1);
   const int64_t blocks = (a.n_units + 255) / 256;
