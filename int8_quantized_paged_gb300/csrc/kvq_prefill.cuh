@@ -81,7 +81,8 @@ __device__ __forceinline__ bool find_tile(const PrefillArgs& a, int x, bool repo
   if (i < 0 || (int64_t)i * a.tq >= n) return false;
   const int L = a.seq_lens[b];
   int bad = 0;
-  if (L < n || (a.ring_rows == 0 && L > (int64_t)a.max_pages * 16)) {
+  // (a position past the last whole step of 2^31 tokens would overflow)
+  if (L < n || L > INT_MAX - 1024 || (a.ring_rows == 0 && L > (int64_t)a.max_pages * 16)) {
     bad = KVQ_DEV_BAD_LEN;
   } else if (a.rope != KVQ_ROPE_NONE && L > a.rope_max_pos) {
     bad = KVQ_DEV_BAD_POS;

@@ -116,10 +116,11 @@ __device__ __forceinline__ float pow2i(int e) {   // 2^e, 0 below 2^-126
 // floats: magnitudes up to x (finite, >= 0) in [2^14, 2^15) ...
 __device__ __forceinline__ int exponent_of(float x) { return (int)(__float_as_uint(x) >> 23) - 127; }
 __device__ __forceinline__ int hold_exponent(float x) { return min(max(exponent_of(x) - 14, -100), 112); }
-// ... and a key's scales up to s in [2^-9, 2^-8) and biases up to b below 2^15
-// (dequant8 multiplies subnormals by 2^24 s).
+// ... and a key's scales up to s in [2^-10, 2^-9) and biases up to b below 2^15.
+// dequant8 multiplies subnormals by 2^24 s, which stays finite even where s is
+// rounded up to 2^-9 (a power of two more, and 2^16 would be infinite).
 __device__ __forceinline__ int key_exponent(float s, float b) {
-  return max(max(exponent_of(s) + 9, exponent_of(b) - 14), -100);
+  return max(max(exponent_of(s) + 10, exponent_of(b) - 14), -100);
 }
 constexpr float kMostScale = 1.0e35f;   // held at 2^126 at most: a larger scale counts as not finite
 __device__ __forceinline__ void group_sync(int id) {
@@ -148,7 +149,7 @@ struct Scale {
   __half2 lo, hi, b;
 };
 template <int KIND>
-__device__ __forceinline__ Scale make_scale(float s, float b) {   // s < 2^-8
+__device__ __forceinline__ Scale make_scale(float s, float b) {   // s < 2^-9
   const __half2 h = __float2half2_rn(s);                           // the stored scale, to fp16
   Scale r;
   r.lo = __hmul2(h, __float2half2_rn(4096.f));                     // 2^24 s, exact
@@ -465,11 +466,19 @@ __device__ void load_queries(const PrefillArgs& a, const PrefillTile& t, int row
       asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(u[0]), "=r"(u[1]) : "r"(at0) : "memory");
       asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(u[2]), "=r"(u[3]) : "r"(at1) : "memory");
       float x[8];
+      if (f16) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 y = __half22float2(u2h(u[i]));
-        x[2 * i] = f16 ? y.x : __uint_as_float(u[i] << 16);
-        x[2 * i + 1] = f16 ? y.y : __uint_as_float(u[i] & 0xFFFF0000u);
+        for (int i = 0; i < 4; ++i) {
+          const float2 y = __half22float2(u2h(u[i]));
+          x[2 * i] = y.x;
+          x[2 * i + 1] = y.y;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[2 * i] = __uint_as_float(u[i] << 16);
+          x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+        }
       }
       if (neox) {
 #pragma unroll

@@ -176,6 +176,29 @@ def test_ranges(key, k_size, v_size):
     c.close()
 
 
+@pytest.mark.parametrize("key", ["llama8b", "llama8b_shimmy", "tiny_f16", "int8_256", "gemma"])
+@pytest.mark.parametrize("below", [0, 1, 2, 4, 8, 16])
+def test_scales_just_below_a_power_of_two(key, below):
+    """The largest scale of a step may round up to the next power of two in fp16."""
+    c = Cache(layer(key), [400])
+    s = c.spec
+    for which, pool in (("k", c.c.k_pool), ("v", c.c.v_pool)):
+        kind, group, param = ((s.k_kind, s.k_group, s.k_param) if which == "k" else (s.v_kind, s.v_group, s.v_param))
+        cb = s.head_dim * (8 if kind == "sym8" else 4) // 8
+        pb = s.head_dim // group * (2 if kind == "affine4" else 1) * (4 if param == "f32" else 2)
+        par = pool.view(-1, s.n_kv_heads, 16 * (cb + pb))[:, :, 16 * cb:]
+        x = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}[param]
+        v = torch.nextafter(torch.tensor(2.0), torch.tensor(0.0)) if below == 0 else torch.tensor(2.0 - below * 2.0 ** -13)
+        vals = par.contiguous().view(x)
+        vals[..., ::2 if kind == "affine4" else 1] = v.to(x).cuda()   # the scales, not the biases
+        par.copy_(vals.view(torch.uint8))
+    q = c.queries(300, size=0.25)
+    out = _prefill(c, q, [300])
+    assert c.c.status_bits() == 0
+    _check(c, q, out, [300], norm=False)
+    c.close()
+
+
 @pytest.mark.parametrize("key", ["llama8b_bf16", "gemma", "llama8b_f16", "tiny"])
 @pytest.mark.parametrize("grow", [True, False])
 def test_values_that_grow_or_shrink_along_the_context(key, grow):
