@@ -45,6 +45,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "kvq_prefill.cuh"
 #include "kvq_prefill_tc.h"
@@ -232,9 +233,9 @@ __device__ void produce(const bool is_v, const PrefillArgs& a, const PrefillTile
   uint32_t raw[NLP * 4];
   float nsc[NS], nbi[AFF ? NS : 1];
   const uint8_t *sub[2] = {pool, pool};   // the pages being loaded
-  int keys = 0;                           // tokens of the step behind the warp's first key
+  int keys[2] = {0, 0};                   // keys below which the pages hold tokens; a bad page holds none
   uint32_t nskip = 0;                     // keys of bad pages
-  auto there = [&](int j) { return j * KPL + kq < keys && !((nskip >> (j * KPL & 16)) & 1u); };
+  auto there = [&](int j) { return j * KPL + kq < keys[j * KPL / P]; };
   auto load_piece = [&](int p) {
 #pragma unroll
     for (int x = 0; x < NLP; ++x) {
@@ -247,24 +248,31 @@ __device__ void produce(const bool is_v, const PrefillArgs& a, const PrefillTile
     }
   };
   auto open_step = [&](int i, const int (&pg)[2]) {   // the pages, and the parameters of the lane's keys
-    keys = i < n ? kr.end(j0 + i) - kr.base<kKeys>(j0 + i) - 32 * warp : 0;
+    const int tokens = i < n ? kr.end(j0 + i) - kr.base<kKeys>(j0 + i) - 32 * warp : 0;
     nskip = 0;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const bool tokens = P * h < keys, ok = pg[h] >= 0 && pg[h] < a.n_pool_pages;
-      if (tokens && !ok) {
+      const bool ok = (uint32_t)pg[h] < (uint32_t)a.n_pool_pages;
+      keys[h] = ok ? tokens : 0;
+      if (__builtin_expect(!ok && P * h < tokens, 0)) {
         nskip |= 0xFFFFu << (P * h);
         if (lane == 0) report(a.status, KVQ_DEV_BAD_PAGE);
       }
       sub[h] = pool + (int64_t)(ok ? pg[h] : 0) * page_bytes;   // some page: its codes meet a scale of 0
     }
     if constexpr (!F16) {
+      const uint8_t* par[2] = {sub[0] + par0 + kq * L.param_row_bytes, sub[1] + par0 + kq * L.param_row_bytes};
+      auto load = [&](auto type) {   // one branch on the type for all
 #pragma unroll
-      for (int j = 0; j < NL; ++j) {
-        const uint8_t* par = sub[j * KPL / P] + par0 + (j * KPL % P + kq) * L.param_row_bytes;
-        nsc[j] = load_param(par, L.param);
-        if constexpr (AFF) nbi[j] = load_param(par + pb, L.param);
-      }
+        for (int j = 0; j < NL; ++j) {
+          const uint8_t* p = par[j * KPL / P] + (j * KPL % P) * L.param_row_bytes;
+          nsc[j] = load_param(p, type.value);
+          if constexpr (AFF) nbi[j] = load_param(p + param_bytes(type.value), type.value);
+        }
+      };
+      if (L.param == KVQ_F32) load(std::integral_constant<int, KVQ_F32>());
+      else if (L.param == KVQ_F16) load(std::integral_constant<int, KVQ_F16>());
+      else load(std::integral_constant<int, KVQ_BF16>());
     }
   };
   // One bit a key of 32 from a vote a load.
@@ -314,31 +322,30 @@ __device__ void produce(const bool is_v, const PrefillArgs& a, const PrefillTile
       return now;
     };
     if constexpr (!F16) {
-      int e = -100;
-      bool odd = false;   // parameters that are not finite, of a key or of what lies behind the keys
+      float ms = 0.f, mb = 0.f;   // the largest scale and bias of the lane's keys
+      bool odd = false;           // parameters that are not finite, of a key or of what lies behind the keys
 #pragma unroll
       for (int j = 0; j < NL; ++j) {
-        const bool fine = nsc[j] < kMostScale && (!AFF || isfinite(nbi[AFF ? j : 0]));
+        const bool fine = nsc[j] < kMostScale && (!AFF || isfinite(nbi[AFF ? j : 0])), on = fine && there(j);
         odd |= !fine;
-        if (fine && there(j)) e = max(e, key_exponent(nsc[j], AFF ? fabsf(nbi[AFF ? j : 0]) : 0.f));
+        sc[j] = on ? nsc[j] : 0.f;
+        ms = fmaxf(ms, sc[j]);
+        if constexpr (AFF) {
+          bi[j] = on ? nbi[j] : 0.f;
+          mb = fmaxf(mb, fabsf(bi[j]));
+        }
       }
       if (__builtin_expect(__any_sync(0xffffffffu, odd), 0)) {
 #pragma unroll
-        for (int j = 0; j < NL; ++j) {
-          const bool fine = nsc[j] < kMostScale && (!AFF || isfinite(nbi[AFF ? j : 0]));
-          bad |= key_bits(j, !fine && there(j));
-          if (!fine) {
-            nsc[j] = 0.f;
-            if constexpr (AFF) nbi[j] = 0.f;
-          }
-        }
+        for (int j = 0; j < NL; ++j)
+          bad |= key_bits(j, !(nsc[j] < kMostScale && (!AFF || isfinite(nbi[AFF ? j : 0]))) && there(j));
       }
-      held = publish(e);
+      held = publish(key_exponent(ms, mb));
       const float down = pow2i(-held);
 #pragma unroll
       for (int j = 0; j < NL; ++j) {
-        sc[j] = there(j) ? nsc[j] * down : 0.f;
-        if constexpr (AFF) bi[j] = there(j) ? nbi[j] * down : 0.f;
+        sc[j] *= down;
+        if constexpr (AFF) bi[j] *= down;
       }
     }
     const int us = i % RU;
