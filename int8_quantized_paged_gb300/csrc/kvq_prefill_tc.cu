@@ -422,32 +422,48 @@ __device__ __forceinline__ void produce_kind(int kind, bool is_v, const PrefillA
   }
 }
 
-// The queries of the CTA's rows, rotated, scaled into fp16 and stored as
-// blocks of 64 dims.  HD / 8 lanes take the heads of a token, one after the
-// other.  The rows are first copied as they are, all at once, and then worked
-// on in place in a short loop: this code runs once a CTA, and what it costs is
-// its latency and its instructions' way into the caches.  Every warp but the
-// producers' takes part, `warp` counted among those.
+// The queries of the CTA's rows, rotated, scaled into fp16 and stored as blocks
+// of 64 dims.  HD / 8 lanes take the heads of a token, one after the other.
+// The rows are first copied as they are, all at once, while the CTA sets itself
+// up, and then worked on in place in a short loop: this code runs once a CTA,
+// and what it costs (a tenth of the time of an 8K prompt) is its latency and
+// its instructions' way into the caches.  Every warp but the producers' takes
+// part, `warp` counted among those.
 template <int HD>
-__device__ void load_queries(const PrefillArgs& a, const PrefillTile& t, int rows, int lg, int kvh, int warp,
-                             int lane, Shared<HD>& sh) {
-  constexpr int HB = HD / 64, LANES = HD / 8, RPW = 32 / LANES, STEP = (4 * row_tiles(HD) + 4) * RPW;
+struct Queries {
+  static constexpr int HB = HD / 64, LANES = HD / 8, RPW = 32 / LANES, STEP = (4 * row_tiles(HD) + 4) * RPW;
+  // Where eight dims from d (a multiple of 8) of row R are.
+  static __device__ __forceinline__ uint32_t chunk(uint32_t base, int R, int d) {
+    return base + ((R >> 7) * HB + d / 64) * kBlockBytes + (R & 127) * 128 + (((d % 64 / 8) ^ (R & 7)) << 4);
+  }
+  static __device__ __forceinline__ int tokens(int rows, int lg) { return (rows + (1 << lg) - 1) >> lg; }
+};
+template <int HD>
+__device__ void copy_queries(const PrefillArgs& a, const PrefillTile& t, int rows, int lg, int kvh, int warp, int lane,
+                             Shared<HD>& sh) {
+  using Q = Queries<HD>;
+  const int li = lane % Q::LANES;
+  const unsigned short* q = static_cast<const unsigned short*>(a.q) + ((int64_t)t.row0 * a.n_heads + (kvh << lg)) * HD;
+#pragma unroll 1
+  for (int k = warp * Q::RPW + lane / Q::LANES; k < Q::tokens(rows, lg); k += Q::STEP)
+#pragma unroll 1
+    for (int h = 0; h < 1 << lg; ++h)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(Q::chunk(smem_u32(sh.q), (k << lg) + h, 8 * li)),
+                   "l"(q + ((int64_t)k * a.n_heads + h) * HD + 8 * li)
+                   : "memory");
+}
+template <int HD>
+__device__ void load_queries(const PrefillArgs& a, const PrefillTile& t, int rows, int lg, int warp, int lane,
+                             Shared<HD>& sh) {
+  using Q = Queries<HD>;
+  constexpr int LANES = Q::LANES, RPW = Q::RPW, STEP = Q::STEP;
   const int li = lane % LANES, first = warp * RPW + lane / LANES;
   const bool neox = a.rope == KVQ_ROPE_NEOX, rope = a.rope != KVQ_ROPE_NONE, f16 = a.act == KVQ_F16;
   const int order = order_of(a.kl.kind);
   const int d0 = neox ? 4 * li : 8 * li, d1 = neox ? HD / 2 + 4 * li : 8 * li + 4;   // two runs of four
-  const int tokens = (rows + (1 << lg) - 1) >> lg;   // rows behind them stay as they are: no result comes from them
+  const int tokens = Q::tokens(rows, lg);   // rows behind them stay as they are: no result comes from them
   const uint32_t base = smem_u32(sh.q);
-  auto row_at = [&](int R) { return base + (R >> 7) * HB * kBlockBytes + (R & 127) * 128; };
-  auto chunk = [&](int R, int d) { return row_at(R) + (d / 64) * kBlockBytes + (((d % 64 / 8) ^ (R & 7)) << 4); };
-  const unsigned short* q = static_cast<const unsigned short*>(a.q) + ((int64_t)t.row0 * a.n_heads + (kvh << lg)) * HD;
-#pragma unroll 1
-  for (int k = first; k < tokens; k += STEP)
-#pragma unroll 1
-    for (int h = 0; h < 1 << lg; ++h)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(chunk((k << lg) + h, 8 * li)),
-                   "l"(q + ((int64_t)k * a.n_heads + h) * HD + 8 * li)
-                   : "memory");
+  auto chunk = [&](int R, int d) { return Q::chunk(base, R, d); };
   auto rotation = [&](int k, float4 (&c)[2]) {   // both pairings meet pairs 4 li .. 4 li + 3
     c[0] = c[1] = make_float4(1.f, 0.f, 1.f, 0.f);
     if (rope && k < tokens) {
@@ -616,7 +632,10 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
   };
 
   constexpr int kMmaWarp = 4 * MT + 8;
+  if (warp < 4 * MT || warp >= kMmaWarp)
+    copy_queries<HD>(a, t, rows, lg, kvh, warp < 4 * MT ? warp : warp - 8, lane, sh);
   if (warp == kMmaWarp) {
+    __syncwarp();
     tmem_alloc(smem_u32(&sh.tmem), kTmemCols);
   } else if (tid == 0) {
     for (int i = 0; i < kStages * 2; ++i) {
@@ -646,7 +665,7 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
   const uint32_t s_col = HD == 256 ? 256 : 0, o_col = HD == 256 ? 0 : 256;
 
   if (warp < 4 * MT || warp >= kMmaWarp) {
-    load_queries<HD>(a, t, rows, lg, kvh, warp < 4 * MT ? warp : warp - 8, lane, sh);
+    load_queries<HD>(a, t, rows, lg, warp < 4 * MT ? warp : warp - 8, lane, sh);
     fence_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(smem_u32(&sh.qfull));
