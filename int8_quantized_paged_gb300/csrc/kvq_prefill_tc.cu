@@ -5,34 +5,34 @@
 // the G heads that share the kv head) over the keys they attend, 128 keys a
 // step:
 //   S = Q' K'^T   (fp16 operands in shared memory, fp32 in tensor memory)
-//   P = 2^(S f - m + 7), rounded to fp16 and written back over S, in one pass
+//   P = 2^(S f - m + 7), rounded to fp16 and written back over S
 //   O += P V'     (P from tensor memory, V' from shared memory)
 // Roles, by warp: MT warpgroups of softmax (a thread owns a row: no shuffles),
-// one warpgroup that dequantizes K and one that dequantizes V (a thread owns a
-// key), and a warp that issues the products.  They meet at
-// mbarriers only.  S comes in halves of 64 keys, two of them in flight per row
-// tile, so that the products of one half run while the softmax works on the
-// other: with a whole step's S in one buffer a row tile's products and softmax
-// took turns.  head_dim 256 has room for one row tile in tensor memory, the
-// others for two.
+// one warpgroup that dequantizes K and one that dequantizes V, and a warp per
+// row tile that issues its products.  They meet at mbarriers only.  S comes in
+// halves of 64 keys, two of them in flight per row tile, so that the products
+// of one half run while the softmax works on the other; head_dim 256 has room
+// for one row tile in tensor memory, the others for two.
 //
 // K' and V' sit in shared memory as blocks of 128 keys x 64 dims in the
-// 128-byte swizzle, in two rings of four blocks.  Codes become exact fp16
-// integers by a mantissa trick, two nibbles of a word at a time, so the dims of
-// every eight are stored in the order 0 4 1 5 2 6 3 7 (4-bit) or, of every
-// four, 0 2 1 3 (8-bit); Q' is stored in the same order and the output is put
-// back in order when it is written.
+// 128-byte swizzle, in two rings of four blocks.  Codes become fp16 values two
+// nibbles (or bytes) of a word at a time, so the dims of every eight are stored
+// in the order 0 4 1 5 2 6 3 7 (4-bit) or, of every four, 0 2 1 3 (8-bit); Q'
+// is stored in the same order and the output is put back in order when it is
+// written.
 //
 // fp16 range.  Operands are fp16 for every activation type: its 11 bits cost a
 // bf16 result nothing, where bf16's 8 would add as much error as the result's
 // own rounding.  A query row, the 128 keys of a step and the values seen so far
-// are each held at a power-of-two scale (chosen from the row's largest element,
-// and from the scales of the step's keys) that puts the largest magnitude in
-// [2^14, 2^15): exact, and free, as the factors go into f, the one multiplier of
-// a row's scores in a step, and into the last scaling of O.  When a step's
-// values are larger than all before, O is rescaled, as it is when the running
-// maximum rises by more than 2^8; P is held times 2^7, which keeps weights down
-// to 2^-21 of the largest in fp16's normal range.
+// are each held at a power-of-two scale (from the row's largest element, and
+// from the scales of the step's keys) that keeps the largest magnitude in
+// fp16's upper range: exact, and free, as the factors go into f, the one
+// multiplier of a row's scores in a step, and into the last scaling of O.  When
+// a step's values are larger than all before, O is rescaled, as it is when the
+// running maximum rises by more than 2^8; P is held times 2^7, which keeps
+// weights down to 2^-21 of the largest in fp16's normal range.  What is rounded
+// to fp16 once: the rotated query, a 32-bit scale, each K^ and V^, each weight.
+// Maxima, sums and O are fp32.
 //
 // Keys that no row may see (behind the last token, bad pages) are zero rows
 // and masked; a key whose scale or element is not finite is a zero row and a
@@ -42,6 +42,17 @@
 // Every wait is bounded (two seconds): when one runs out the CTA runs through
 // its remaining steps without waiting, frees its tensor memory and reports
 // KVQ_DEV_TIMEOUT.
+//
+// Measured, Llama-shaped layer (32 / 8 heads of 128, 4-bit K and V): an 8K
+// prompt 0.545 ms, 1.01 PFLOP/s of causal products, 52 % of the measured
+// matrix rate.  Tensor pipe active 42 %, issue slots 60 % with four to five
+// warps a scheduler: bound by the instructions of softmax and dequantization
+// (11,400 a step of 256 rows x 128 keys; the products alone would take 2500
+// cycles of about 4000), and for a sixth of the time by a CTA's start and end,
+// which nothing overlaps as a CTA fills its SM.  What was tried: a step's S in
+// one buffer, 722 us where two halves took 640; products 128 keys wide, 653
+// against 545; two threads a row or a warpgroup per half (more warps, more
+// instructions), 777 and 610 against 722 and 555.
 #include <cuda_runtime.h>
 
 #include <atomic>
@@ -69,6 +80,8 @@ __host__ __device__ constexpr int tc_threads(int hd) { return 128 * row_tiles(hd
 // Registers a thread: at launch (65536 over the threads, in eights), then by
 // role.  A role may only take what the others gave back, so the shares must
 // not exceed the launch's: (softmax * tiles + 2 producers + products) * 128.
+// Eight fewer for the softmax and it spills (8K prompt 545 -> 582 us); eight
+// fewer for the producers and they do (f16 rows 1.22 -> 1.30 ms).
 __host__ __device__ constexpr int regs_launch(int hd) { return 65536 / tc_threads(hd) / 8 * 8; }
 __host__ __device__ constexpr int regs_softmax(int hd) { return hd == 256 ? 184 : 136; }
 __host__ __device__ constexpr int regs_produce(int hd) { return hd == 256 ? 128 : 88; }

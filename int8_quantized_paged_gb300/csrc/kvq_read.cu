@@ -8,10 +8,13 @@
 // kvq_append.cu); pages: [airllm] §2.3.
 //
 // A thread owns 16 consecutive elements of one row of one kv head (every scale
-// group is a multiple of 16, so they share one scale) of K and of V: its loads
-// are independent, and consecutive threads write consecutive 16-byte pieces of
-// the outputs, which are most of the bytes (4 times the codes' at 4 bits and a
-// 16-bit activation type).
+// group is a multiple of 16, so they share one scale) of K, then of V.  Bound
+// by the latency of four dependent steps (position, table, codes, store), so by
+// the threads in flight: 32 registers, eight blocks an SM.  The outputs are
+// most of the bytes (4 times the codes' at 4 bits and a 16-bit type), and 32
+// bytes a store write whole sectors: four 64K contexts of 8-bit K and 4-bit V
+// as fp16, 757 MB, 155 us, 4.9 TB/s or 73 % of the measured copy rate; 166 us
+// in two stores of 16 bytes.  A block that looks its rows up first, 157 to 167.
 #include <cuda_runtime.h>
 
 #include "kvq_device.cuh"
