@@ -82,18 +82,28 @@ class LayerCache:
                                     self.block_table, self.max_pages, seq_lens, self.rope_tab, self.rope_max_pos,
                                     out, workspace, self.status, chunk_tokens, stream)
 
+    def _plain_ring(self) -> None:
+        if self.sinks and self.ring_rows:   # its ring starts behind the pinned pages
+            raise ValueError("a ring behind pinned first tokens is decoded with sink_decode or append_sink_decode")
+
     def append_window_decode(self, q, k_new, v_new, pos, seq_lens, out, workspace, window: int,
                              chunk_tokens: int = 0, stream=None) -> None:
         """Append row b at pos[b] into the ring of every sequence b, then window-decode (one call)."""
+        self._plain_ring()
         kvq.append_window_decode(self.cfg, q, k_new, v_new, pos, self.k_pool, self.v_pool, self.n_pool_pages,
                                  self.block_table, self.ring_rows, window, seq_lens, self.rope_tab,
                                  self.rope_max_pos, out, workspace, self.status, chunk_tokens, stream)
 
     def window_decode(self, q, seq_lens, out, workspace, window: int, chunk_tokens: int = 0,
                       stream=None) -> None:
+        self._plain_ring()
         kvq.window_decode(self.cfg, q, self.k_pool, self.v_pool, self.n_pool_pages, self.block_table,
                           self.ring_rows, window, seq_lens, self.rope_tab, self.rope_max_pos, out, workspace,
                           self.status, chunk_tokens, stream)
+
+    def _like(self, out, shape) -> None:
+        if out.dtype != self.act_dtype or tuple(out.shape) != tuple(shape):
+            raise ValueError(f"tensor is {out.dtype} {tuple(out.shape)}, not {self.act_dtype} {tuple(shape)}")
 
     def read(self, pos, seq_ids=None, k_out=None, v_out=None, stream=None):
         """(K, V) rows of tokens pos[i] of sequences seq_ids[i] as numbers: [n][kv heads][head_dim]."""
@@ -102,6 +112,8 @@ class LayerCache:
             k_out = torch.empty(shape, dtype=self.act_dtype, device=self.device)
         if v_out is None:
             v_out = torch.empty(shape, dtype=self.act_dtype, device=self.device)
+        self._like(k_out, shape)
+        self._like(v_out, shape)
         kvq.read(self.cfg, seq_ids, pos, self.block_table, self.n_seqs, self.max_pages, self.ring_rows, self.sinks,
                  self.k_pool, self.v_pool, self.n_pool_pages, k_out, v_out, self.status, stream)
         return k_out, v_out
@@ -130,6 +142,10 @@ class LayerCache:
 
     def prefill(self, q, q_starts, seq_lens, out, workspace, window: int = 0, stream=None) -> None:
         """Causal attention of the last tokens of every sequence; with a window the cache's sinks stay visible."""
+        self._like(q, (q.shape[0], self.cfg.n_heads, self.cfg.head_dim))
+        self._like(out, q.shape)
+        if q_starts.shape[0] != seq_lens.shape[0] + 1:
+            raise ValueError("q_starts has one entry more than seq_lens")
         kvq.prefill_attention(self.cfg, q, q_starts, self.k_pool, self.v_pool, self.n_pool_pages, self.block_table,
                               self.max_pages, self.ring_rows, self.sinks if window else 0, window, seq_lens,
                               self.rope_tab, self.rope_max_pos, out, workspace, self.status, stream)

@@ -136,3 +136,26 @@ def test_workspace_sizes():
         a = {**dict(batch=1, max_pages_per_seq=8, ring_rows=0, sinks=0, window=8, chunk_tokens=0), **bad}
         with pytest.raises(kvq.KvqError):
             kvq.sink_workspace_bytes(c, **a)
+
+
+def test_layer_cache_refusals():
+    """Calls whose tensors or layout do not fit are refused before anything is launched."""
+    from int8_quantized_paged_gb300.cache import LayerCache
+    c = LayerCache(_cfg(), 1, 8, 8, rope_max_pos=64, ring_rows=32, device="cpu", sinks=4)
+    i32 = lambda n: torch.zeros(n, dtype=torch.int32)   # noqa: E731
+    rows = lambda n, h=32, t=torch.float16: torch.zeros(n, h, 128, dtype=t)   # noqa: E731
+    ws = torch.zeros(64, dtype=torch.uint8)
+    # a ring behind pinned pages is not the ring that the plain window decode reads
+    with pytest.raises(ValueError, match="sink_decode"):
+        c.window_decode(rows(1), i32(1), rows(1), ws, 16)
+    with pytest.raises(ValueError, match="sink_decode"):
+        c.append_window_decode(rows(1), rows(1, 8), rows(1, 8), i32(1), i32(1), rows(1), ws, 16)
+    for k, v in ((rows(2, 8), rows(3, 8)), (rows(3, 8, torch.float32), None), (rows(3, 4), None)):
+        with pytest.raises(ValueError, match="tensor is"):
+            c.read(i32(3), k_out=k, v_out=v)
+    for q, out in ((rows(3), rows(2)), (rows(3), rows(3, t=torch.bfloat16)), (rows(3, 8), rows(3, 8))):
+        with pytest.raises(ValueError, match="tensor is"):
+            c.prefill(q, i32(2), i32(1), out, ws, 16)
+    with pytest.raises(ValueError, match="q_starts"):
+        c.prefill(rows(3), i32(3), i32(1), rows(3), ws, 16)
+    c.close()
