@@ -71,7 +71,7 @@ __device__ __forceinline__ bool find_tile(const PrefillArgs& a, int x, bool repo
     else hi = mid - 1;
   }
   const int b = lo;
-  const int s0 = a.q_starts[b], s1 = a.q_starts[b + 1];
+  const int s0 = a.q_starts[b], s1 = a.q_starts[b + 1], L = a.seq_lens[b];
   if (s0 < 0 || s1 < s0 || s1 > a.n_rows) {
     if (reporter) report(a.status, KVQ_DEV_BAD_SEQ);
     return false;
@@ -79,7 +79,6 @@ __device__ __forceinline__ bool find_tile(const PrefillArgs& a, int x, bool repo
   const int n = s1 - s0;
   const int i = x - (s0 / a.tq + b);
   if (i < 0 || (int64_t)i * a.tq >= n) return false;
-  const int L = a.seq_lens[b];
   int bad = 0;
   // (a position past the last whole step of 2^31 tokens would overflow)
   if (L < n || L > INT_MAX - 1024 || (a.ring_rows == 0 && L > (int64_t)a.max_pages * 16)) {

@@ -44,11 +44,11 @@
 // KVQ_DEV_TIMEOUT.
 //
 // Measured, Llama-shaped layer (32 / 8 heads of 128, 4-bit K and V): an 8K
-// prompt 0.545 ms, 1.01 PFLOP/s of causal products, 52 % of the measured
+// prompt 0.537 ms, 1.02 PFLOP/s of causal products, 52 % of the measured
 // matrix rate.  Tensor pipe active 42 %, issue slots 60 % with four to five
 // warps a scheduler: bound by the instructions of softmax and dequantization
 // (11,400 a step of 256 rows x 128 keys; the products alone would take 2500
-// cycles of about 4000), and for a sixth of the time by a CTA's start and end,
+// cycles of about 4000), and for a seventh of the time by a CTA's start and end,
 // which nothing overlaps as a CTA fills its SM.  What was tried: a step's S in
 // one buffer, 722 us where two halves took 640; products 128 keys wide, 653
 // against 545; two threads a row or a warpgroup per half (more warps, more
@@ -76,6 +76,12 @@ constexpr float kLazy = 8.0f;            // the running maximum rises past +2^8 
 constexpr float kShift = 7.0f;           // P is held times 2^7
 
 __host__ __device__ constexpr int row_tiles(int hd) { return hd == 256 ? 1 : 2; }
+// Tensor memory has 512 columns: S 128 and O head_dim a row tile.  Where the
+// queries fit beside them (not at head_dim 128) the scores' products take them
+// from there: from shared memory a product of 128 x 64 x 16 reads 6 KB in the
+// time that moves 4 (window layer of head_dim 256: 209 -> 207 us).
+template <int HD>
+constexpr bool kQInTmem = HD != 128;
 __host__ __device__ constexpr int tc_threads(int hd) { return 128 * row_tiles(hd) + 256 + 128; }
 // Registers a thread: at launch (65536 over the threads, in eights), then by
 // role.  A role may only take what the others gave back, so the shares must
@@ -116,7 +122,7 @@ struct Shared {
   uint64_t qfull;                        // the queries are there
   uint64_t sfull[MT][2], pfull[MT][2];   // scores and weights of a half step
   uint64_t ofull[MT][2];                 // O with it
-  uint64_t drain[MT];
+  uint64_t qtmem[MT], drain[MT];
   uint32_t tmem;
   int stop;
 };
@@ -127,9 +133,10 @@ __device__ __forceinline__ float pow2i(int e) {   // 2^e, 0 below 2^-126
   return e < -126 ? 0.f : __int_as_float((e + 127) << 23);
 }
 // Exponents at which operands are held, as far as both factors stay normal
-// floats: magnitudes up to x (finite, >= 0) in [2^14, 2^15) ...
+// floats: magnitudes up to x (finite, >= 0) in [2^14, 2^15) ...  For a query x is
+// sqrt 2 times its largest element, the most that a rotated one can be.
 __device__ __forceinline__ int exponent_of(float x) { return (int)(__float_as_uint(x) >> 23) - 127; }
-__device__ __forceinline__ int hold_exponent(float x) { return min(max(exponent_of(x) - 14, -100), 112); }
+__device__ __forceinline__ int hold_exponent(float x) { return min(max(exponent_of(x) - 14, -100), 114); }
 // ... and a key's scales up to s in [2^-10, 2^-9) and biases up to b below 2^15.
 // dequant8 multiplies subnormals by 2^24 s, which stays finite even where s is
 // rounded up to 2^-9 (a power of two more, and 2^16 would be infinite).
@@ -152,10 +159,6 @@ __host__ __device__ constexpr int order_of(int kind) {
 // The dim (0..7) at position i of an ordered group of eight.
 __host__ __device__ constexpr int dim_at(int order, int i) {
   return order == 0 ? i : (order == 1 ? (i & 4) | ((i & 1) << 1) | ((i >> 1) & 1) : (i >> 1) | ((i & 1) << 2));
-}
-// The position of dim d of eight.
-__host__ __device__ constexpr int pos_of(int order, int d) {
-  return order == 0 ? d : (order == 1 ? (d & 4) | ((d & 1) << 1) | ((d >> 1) & 1) : ((d & 3) << 1) | (d >> 2));
 }
 
 // A group's scale and bias for dequant8.
@@ -436,137 +439,163 @@ __device__ __forceinline__ void produce_kind(int kind, bool is_v, const PrefillA
 }
 
 // The queries of the CTA's rows, rotated, scaled into fp16 and stored as blocks
-// of 64 dims.  HD / 8 lanes take the heads of a token, one after the other.
-// The rows are first copied as they are, all at once, while the CTA sets itself
-// up, and then worked on in place in a short loop: this code runs once a CTA,
-// and what it costs (a tenth of the time of an 8K prompt) is its latency and
-// its instructions' way into the caches.  Every warp but the producers' takes
-// part, `warp` counted among those.
+// of 64 dims.  HD / 8 lanes take a row, a 16-byte chunk of it each.  The rows
+// are first copied as they are, all at once, while the CTA sets itself up, and
+// then worked on in place, two of a lane's at once, or four where the launch
+// has 128 registers (head_dim 256; with 96 four spill in the steps: 8K prompt
+// 545 -> 564 us; window layer 202 us with two, 200 with four).  This runs once a
+// CTA and costs the latency of its instructions: 13,000 cycles of 162,000 in an
+// 8K prompt before a row's exponent was taken from its stored bits, two rows in
+// a word (543 -> 537 us; window layer 207 -> 200).  Every warp but the producers'
+// takes part, `warp` counted among those.
 template <int HD>
 struct Queries {
-  static constexpr int HB = HD / 64, LANES = HD / 8, RPW = 32 / LANES, STEP = (4 * row_tiles(HD) + 4) * RPW;
+  static constexpr int HB = HD / 64, LANES = HD / 8, kRows = HD == 256 ? 4 : 2;
+  static constexpr int WARP = 32 / LANES * kRows, STEP = (4 * row_tiles(HD) + 4) * WARP;   // rows of a warp, of all
+  // The lane's eight dims: with NeoX pairing lanes 2 i and 2 i + 1 have the
+  // i-th chunks of the two halves, the pairs of eight positions between them.
+  static __device__ __forceinline__ int dim(int li, bool neox) {
+    return neox ? 8 * (li >> 1) + (li & 1) * (HD / 2) : 8 * li;
+  }
   // Where eight dims from d (a multiple of 8) of row R are.
   static __device__ __forceinline__ uint32_t chunk(uint32_t base, int R, int d) {
     return base + ((R >> 7) * HB + d / 64) * kBlockBytes + (R & 127) * 128 + (((d % 64 / 8) ^ (R & 7)) << 4);
   }
-  static __device__ __forceinline__ int tokens(int rows, int lg) { return (rows + (1 << lg) - 1) >> lg; }
 };
 template <int HD>
 __device__ void copy_queries(const PrefillArgs& a, const PrefillTile& t, int rows, int lg, int kvh, int warp, int lane,
                              Shared<HD>& sh) {
   using Q = Queries<HD>;
-  const int li = lane % Q::LANES;
-  const unsigned short* q = static_cast<const unsigned short*>(a.q) + ((int64_t)t.row0 * a.n_heads + (kvh << lg)) * HD;
+  const int d = Q::dim(lane % Q::LANES, a.rope == KVQ_ROPE_NEOX);
+  const uint32_t base = smem_u32(sh.q);
+  const unsigned short* q =
+      static_cast<const unsigned short*>(a.q) + ((int64_t)t.row0 * a.n_heads + (kvh << lg)) * HD + d;
 #pragma unroll 1
-  for (int k = warp * Q::RPW + lane / Q::LANES; k < Q::tokens(rows, lg); k += Q::STEP)
-#pragma unroll 1
-    for (int h = 0; h < 1 << lg; ++h)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(Q::chunk(smem_u32(sh.q), (k << lg) + h, 8 * li)),
-                   "l"(q + ((int64_t)k * a.n_heads + h) * HD + 8 * li)
-                   : "memory");
+  for (int R0 = warp * Q::WARP + lane / Q::LANES * Q::kRows; R0 < rows; R0 += Q::STEP)
+#pragma unroll
+    for (int u = 0; u < Q::kRows; ++u) {
+      const int R = R0 + u;
+      if (R < rows)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(Q::chunk(base, R, d)),
+                     "l"(q + ((int64_t)(R >> lg) * a.n_heads + (R & ((1 << lg) - 1))) * HD)
+                     : "memory");
+    }
 }
 template <int HD>
 __device__ void load_queries(const PrefillArgs& a, const PrefillTile& t, int rows, int lg, int warp, int lane,
                              Shared<HD>& sh) {
   using Q = Queries<HD>;
-  constexpr int LANES = Q::LANES, RPW = Q::RPW, STEP = Q::STEP;
-  const int li = lane % LANES, first = warp * RPW + lane / LANES;
+  constexpr int U = Q::kRows;
+  const int li = lane % Q::LANES;
   const bool neox = a.rope == KVQ_ROPE_NEOX, rope = a.rope != KVQ_ROPE_NONE, f16 = a.act == KVQ_F16;
-  const int order = order_of(a.kl.kind);
-  const int d0 = neox ? 4 * li : 8 * li, d1 = neox ? HD / 2 + 4 * li : 8 * li + 4;   // two runs of four
-  const int tokens = Q::tokens(rows, lg);   // rows behind them stay as they are: no result comes from them
+  const bool odd = li & 1;
+  const int d = Q::dim(li, neox), order = order_of(a.kl.kind);
+  // Ordered words of dims 01 23 45 67: pairs of words, the low and the high halves.
+  const bool swap = order != 2;
+  const uint32_t lows = order == 0 ? 0x3210 : 0x5410, highs = order == 0 ? 0x7654 : 0x7632;
   const uint32_t base = smem_u32(sh.q);
-  auto chunk = [&](int R, int d) { return Q::chunk(base, R, d); };
-  auto rotation = [&](int k, float4 (&c)[2]) {   // both pairings meet pairs 4 li .. 4 li + 3
-    c[0] = c[1] = make_float4(1.f, 0.f, 1.f, 0.f);
-    if (rope && k < tokens) {
-      const float4* p = reinterpret_cast<const float4*>(a.rope_tab + ((int64_t)(t.p0 + k) * (HD / 2) + 4 * li) * 2);
-      c[0] = p[0];
-      c[1] = p[1];
-    }
+  // both pairings meet pairs 4 li .. 4 li + 3
+  const float4* rot = reinterpret_cast<const float4*>(a.rope_tab) + (int64_t)t.p0 * (HD / 4) + 2 * li;
+  // The halves of two lanes' chunks change hands: NeoX positions 0..3 and 4..7 of their 16.
+  auto exchange = [&](uint32_t (&w)[4]) {
+    const uint32_t r0 = __shfl_xor_sync(0xffffffffu, odd ? w[0] : w[2], 1);
+    const uint32_t r1 = __shfl_xor_sync(0xffffffffu, odd ? w[1] : w[3], 1);
+    if (odd) w[0] = r0, w[1] = r1;
+    else w[2] = r0, w[3] = r1;
   };
-  float4 nc[2];
-  rotation(first, nc);
-  asm volatile("cp.async.wait_all;" ::: "memory");
-  __syncwarp();
+  bool copied = false;
 #pragma unroll 1
-  for (int k = first; k - lane / LANES < tokens; k += STEP) {   // the same count for every lane of a warp
-    const bool there = k < tokens;
-    const float c[4] = {nc[0].x, nc[0].z, nc[1].x, nc[1].z}, s[4] = {nc[0].y, nc[0].w, nc[1].y, nc[1].w};
-    rotation(k + STEP, nc);
-#pragma unroll 1
-    for (int h = 0; h < 1 << lg; ++h) {
-      const int R = ((there ? k : 0) << lg) + h;
-      const uint32_t at0 = chunk(R, d0) + 2 * (d0 & 7), at1 = chunk(R, d1) + 2 * (d1 & 7);
-      uint32_t u[4];
-      asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(u[0]), "=r"(u[1]) : "r"(at0) : "memory");
-      asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(u[2]), "=r"(u[3]) : "r"(at1) : "memory");
-      float x[8];
+  for (int Rw = warp * Q::WARP; Rw < rows; Rw += Q::STEP) {   // the same count for every lane of a warp
+    const int R0 = Rw + lane / Q::LANES * U;
+    float4 c[U][2];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      c[u][0] = c[u][1] = make_float4(1.f, 0.f, 1.f, 0.f);
+      if (rope && R0 + u < rows) {
+        const float4* p = rot + (int64_t)((R0 + u) >> lg) * (HD / 4);
+        c[u][0] = p[0];
+        c[u][1] = p[1];
+      }
+    }
+    if (!copied) asm volatile("cp.async.wait_all;" ::: "memory");   // a lane's own chunks
+    copied = true;
+    // (rows behind the last take part: nothing comes of them)
+    // A row's largest element, as bits of the activation type (magnitudes are in
+    // the order of their bits; a NaN is above all, and its row NaN whatever its
+    // scale): two rows in a word.  A rotated element is at most sqrt 2 of it.
+    uint32_t w[U][4], top[U / 2];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(w[u][0]), "=r"(w[u][1]), "=r"(w[u][2]), "=r"(w[u][3])
+                   : "r"(Q::chunk(base, R0 + u, d))
+                   : "memory");
+#pragma unroll
+    for (int v = 0; v < U / 2; ++v) {
+      uint32_t m[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t(&y)[4] = w[2 * v + k];
+        constexpr uint32_t mag = 0x7FFF7FFFu;
+        m[k] = __vmaxu2(__vmaxu2(y[0] & mag, y[1] & mag), __vmaxu2(y[2] & mag, y[3] & mag));
+      }
+      top[v] = __vmaxu2(__byte_perm(m[0], m[1], 0x5410), __byte_perm(m[0], m[1], 0x7632));
+    }
+#pragma unroll
+    for (int o = Q::LANES / 2; o >= 1; o >>= 1)
+#pragma unroll
+      for (int v = 0; v < U / 2; ++v) top[v] = __vmaxu2(top[v], __shfl_xor_sync(0xffffffffu, top[v], o));
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t bits = u & 1 ? top[u / 2] >> 16 : top[u / 2] & 0xFFFFu;
+      const float most = f16 ? __half2float(__ushort_as_half((unsigned short)bits)) : __uint_as_float(bits << 16);
+      const int e = hold_exponent(1.4142137f * most);
+      const float down = pow2i(-e);
+      if (neox) exchange(w[u]);
+      float y[8], x[8];
       if (f16) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float2 y = __half22float2(u2h(u[i]));
-          x[2 * i] = y.x;
-          x[2 * i + 1] = y.y;
+          const float2 z = __half22float2(u2h(w[u][i]));
+          y[2 * i] = z.x;
+          y[2 * i + 1] = z.y;
         }
       } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          x[2 * i] = __uint_as_float(u[i] << 16);
-          x[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+          y[2 * i] = __uint_as_float(w[u][i] << 16);
+          y[2 * i + 1] = __uint_as_float(w[u][i] & 0xFFFF0000u);
         }
       }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] *= down;
+      const float co[4] = {c[u][0].x, c[u][0].z, c[u][1].x, c[u][1].z};
+      const float si[4] = {c[u][0].y, c[u][0].w, c[u][1].y, c[u][1].w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = y[i];
       if (neox) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float p = x[i], m = x[4 + i];
-          x[i] = p * c[i] - m * s[i];
-          x[4 + i] = p * s[i] + m * c[i];
+          x[i] = y[i] * co[i] - y[4 + i] * si[i];
+          x[4 + i] = y[i] * si[i] + y[4 + i] * co[i];
         }
       } else if (rope) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float p = x[2 * i], m = x[2 * i + 1];
-          x[2 * i] = p * c[i] - m * s[i];
-          x[2 * i + 1] = p * s[i] + m * c[i];
+          x[2 * i] = y[2 * i] * co[i] - y[2 * i + 1] * si[i];
+          x[2 * i + 1] = y[2 * i] * si[i] + y[2 * i + 1] * co[i];
         }
       }
-      float top = 0.f;
+      uint32_t n[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(x[i]));
-#pragma unroll
-      for (int o = LANES / 2; o >= 1; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const int e = hold_exponent(top);
-      const float down = pow2i(-e);
-      __syncwarp();   // the lane that shares a chunk has read it
-      if (!there) continue;
-      if (li == 0) sh.qscale[R] = a.score_scale * pow2i(e);
-      auto word = [&](int i, int k) { return h2u(__floats2half2_rn(x[i] * down, x[k] * down)); };
-      if (!neox) {   // the lane's eight dims are one chunk
-        uint32_t w[4];
-        if (order == 2) {
-          w[0] = word(0, 4), w[1] = word(1, 5), w[2] = word(2, 6), w[3] = word(3, 7);
-        } else if (order == 1) {
-          w[0] = word(0, 2), w[1] = word(1, 3), w[2] = word(4, 6), w[3] = word(5, 7);
-        } else {
-          w[0] = word(0, 1), w[1] = word(2, 3), w[2] = word(4, 5), w[3] = word(6, 7);
-        }
-        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at0), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
-                     : "memory");
-      } else {   // two runs of four dims: each half a chunk, or every other half of one
-#pragma unroll
-        for (int i = 0; i < 8; i += 2) {
-          const uint32_t w = word(i, i + 1);
-          const int d = (i < 4 ? d0 : d1) + i % 4;
-          const uint32_t at = chunk(R, d);
-          asm volatile("st.shared.b16 [%0], %1;" ::"r"(at + 2 * pos_of(order, d & 7)),
-                       "h"((unsigned short)(w & 0xFFFFu))
-                       : "memory");
-          asm volatile("st.shared.b16 [%0], %1;" ::"r"(at + 2 * pos_of(order, (d + 1) & 7)),
-                       "h"((unsigned short)(w >> 16))
-                       : "memory");
-        }
-      }
+      for (int i = 0; i < 4; ++i) n[i] = h2u(__floats2half2_rn(x[2 * i], x[2 * i + 1]));
+      if (neox) exchange(n);
+      const uint32_t n1 = swap ? n[2] : n[1], n2 = swap ? n[1] : n[2];
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(Q::chunk(base, R0 + u, d)),
+                   "r"(__byte_perm(n[0], n2, lows)), "r"(__byte_perm(n[0], n2, highs)),
+                   "r"(__byte_perm(n1, n[3], lows)), "r"(__byte_perm(n1, n[3], highs))
+                   : "memory");
+      if (li == 0) sh.qscale[R0 + u] = a.score_scale * pow2i(e);
     }
   }
 }
@@ -667,6 +696,7 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
         mbar_init(smem_u32(&sh.pfull[i][h]), 4);
         mbar_init(smem_u32(&sh.ofull[i][h]), 1);
       }
+      mbar_init(smem_u32(&sh.qtmem[i]), 4);
       mbar_init(smem_u32(&sh.drain[i]), 1);
     }
     sh.stop = 0;
@@ -676,6 +706,7 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
   const uint32_t s_col = HD == 256 ? 256 : 0, o_col = HD == 256 ? 0 : 256;
+  constexpr uint32_t q_col = 384;   // kQInTmem
 
   if (warp < 4 * MT || warp >= kMmaWarp) {
     load_queries<HD>(a, t, rows, lg, warp < 4 * MT ? warp : warp - 8, lane, sh);
@@ -698,6 +729,24 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
       const int nh = half_steps(rt);
       float m = -INFINITY, l = 0.f, f = 0.f;
       int held = 0, tb = 0, end = 0, ve = 0;
+      if constexpr (kQInTmem<HD>) {   // the row's queries, a dim pair a column
+        const uint32_t q_at = smem_u32(sh.q) + rt * HB * kBlockBytes;
+#pragma unroll 1
+        for (int d = 0; d < HD; d += 32) {
+          uint32_t w[16];
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[4 * c]), "=r"(w[4 * c + 1]), "=r"(w[4 * c + 2]), "=r"(w[4 * c + 3])
+                         : "r"(q_at + (d / 64) * kBlockBytes + (R & 127) * 128 + (((d / 8 + c) % 8 ^ (R & 7)) << 4))
+                         : "memory");
+          tmem_st16(tmem + lanes + q_col + rt * (HD / 2) + d / 2, w);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.qtmem[rt]));
+      }
       bool whole = false;
 #pragma unroll 1
       for (int u = 0; u < nh; ++u) {
@@ -888,6 +937,7 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
       const int nh = __shfl_sync(0xffffffffu, half_steps(rt), 0);
       const uint32_t s_at = __shfl_sync(0xffffffffu, tmem, 0) + s_col + rt * 128;
       const uint32_t o_at = __shfl_sync(0xffffffffu, tmem, 0) + o_col + rt * HD;
+      const uint32_t q_at = __shfl_sync(0xffffffffu, tmem, 0) + q_col + rt * (HD / 2);
       auto qk = [&](int u) {   // scores of half step u
         const int i = u >> 1, hf = u & 1, us = i % RU;
         mbar_wait(smem_u32(&sh.kfull[us][hf]), (i / RU) & 1, stop);
@@ -896,8 +946,11 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
           const uint64_t b = kd + (us * HB * kBlockBytes + hf * kHalfBytes) / 16;
 #pragma unroll
           for (int k = 0; k < 4 * HB; ++k)
-            mma_ss(s_at + hf * 64, qd + ((k / 4) * kBlockBytes + 32 * (k % 4)) / 16,
-                   b + ((k / 4) * kBlockBytes + 32 * (k % 4)) / 16, id_qk, k > 0);
+            if constexpr (kQInTmem<HD>)
+              mma_ts(s_at + hf * 64, q_at + 8 * k, b + ((k / 4) * kBlockBytes + 32 * (k % 4)) / 16, id_qk, k > 0);
+            else
+              mma_ss(s_at + hf * 64, qd + ((k / 4) * kBlockBytes + 32 * (k % 4)) / 16,
+                     b + ((k / 4) * kBlockBytes + 32 * (k % 4)) / 16, id_qk, k > 0);
           mma_commit(smem_u32(&sh.kempty[us][hf]));
           mma_commit(smem_u32(&sh.sfull[rt][hf]));
         }
@@ -919,6 +972,7 @@ __global__ void __launch_bounds__(tc_threads(HD), 1) prefill_tc_kernel(const __g
         __syncwarp();
       };
       // Scores run two half steps ahead of the weights, in two buffers.
+      if constexpr (kQInTmem<HD>) mbar_wait(smem_u32(&sh.qtmem[rt]), 0, stop);   // (each wait has its fence behind it)
       if (nh > 0) qk(0);
       if (nh > 1) qk(1);
 #pragma unroll 1
