@@ -44,10 +44,10 @@
 // KVQ_DEV_TIMEOUT.
 //
 // Measured, Llama-shaped layer (32 / 8 heads of 128, 4-bit K and V): an 8K
-// prompt 0.537 ms, 1.02 PFLOP/s of causal products, 52 % of the measured
-// matrix rate.  Tensor pipe active 42 %, issue slots 60 % with four to five
+// prompt 0.537 ms, 1.02 PFLOP/s of causal products, 53 % of the measured
+// matrix rate.  Tensor pipe active 43 %, issue slots 60 % with four to five
 // warps a scheduler: bound by the instructions of softmax and dequantization
-// (11,400 a step of 256 rows x 128 keys; the products alone would take 2500
+// (11,100 a step of 256 rows x 128 keys; the products alone would take 2500
 // cycles of about 4000), and for a seventh of the time by a CTA's start and end,
 // which nothing overlaps as a CTA fills its SM.  What was tried: a step's S in
 // one buffer, 722 us where two halves took 640; products 128 keys wide, 653
