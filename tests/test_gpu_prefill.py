@@ -413,3 +413,32 @@ def test_a_session(key):
         assert np.all(np.abs(x.double().cpu().numpy() - ref) <= (2.0 ** -23 + half) * np.abs(ref) + 2.0 ** -25)
     assert c.c.status_bits() == 0
     c.close()
+
+
+@pytest.mark.parametrize("key", ["llama8b", "llama8b_bf16", "gemma", "gemma_bf16", "tiny_f16", "tiny", "g1"])
+@pytest.mark.parametrize("n", [1, 2, 131])
+def test_largest_queries(key, n):
+    """Queries at fp16's upper end, which pass it when rotated, beside rows of zeros; a query that is
+    not finite makes its own row NaN and no other."""
+    top = 6.5e4
+    w = layer(key)
+    # scores of about N(0, 1) (2 with score scale 1), as in the other tests
+    c = Cache(w, [max(n, 40) + 60], k_size=1.0 / top / (8.0 if w["attn_scale"] else 1.0))
+    q = torch.sign(c.queries(n).float()).mul(top).to(c.act)
+    q[1::3] = 0
+    L = c.lens[0]
+    out = _prefill(c, q, [n])
+    assert c.c.status_bits() == 0
+    pools = c.pools()
+    _near(c, pools, out, q, 0, np.arange(L - n, L), 0)
+    if n > 100:
+        heads, hd = w["n_heads"], w["head_dim"]
+        for i, x in ((5, "nan"), (6, "inf"), (77, "-inf")):
+            q[i, i % heads, i % hd] = float(x)
+        got = _prefill(c, q, [n])
+        bad = torch.zeros(n, heads, dtype=torch.bool, device="cuda")
+        for i in (5, 6, 77):
+            bad[i, i % heads] = True
+        assert torch.isnan(got[bad]).all()
+        assert torch.equal(got[~bad], out[~bad])
+    c.close()
